@@ -316,6 +316,73 @@ int slim_dequant_gemv(const uint32_t* codes, const uint8_t* bits, const float* s
                       int64_t batch, float* y, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * slim_dequant_grouped_gemm: Y_e = X_e W_hat_e^T for E packed layers of one
+ * shape (the experts of a mixture; E = 1: one layer), any number of rows, the
+ * rows sorted by expert and the counts known on the device only. W_hat_e is
+ * slim_dequant_gemv's, per expert.
+ *   codes    device E x m x slim_row_words(n, avg_bits) uint32, 16-byte aligned.
+ *   bits     device E x k uint8, each expert's in 1..8 and summing to
+ *            k * avg_bits (the caller's precondition: no word outside a row is
+ *            read whatever bits holds, but that expert's y is then unspecified).
+ *   scale, zero  device E x m x k float32.
+ *   x        device T x n, row-major, float32 or bf16 (xdtype), 16-byte
+ *            aligned. Values must be finite: an infinity or NaN makes its own
+ *            row of y NaN or infinite, and no other row.
+ *   row_index  device R int32, or NULL. Grouped row r reads row row_index[r]
+ *            of x (row r when NULL; then T >= R). The same row of x may be read
+ *            by many grouped rows; an index outside [0, T) reads as zeros.
+ *   offsets  device E + 1 int32, non-decreasing: expert e's grouped rows are
+ *            offsets[e] <= r < offsets[e + 1] (none when equal). Values are
+ *            clamped to [0, R]; rows of y that belong to no expert (before
+ *            offsets[0], behind offsets[E]) are not written.
+ *   y        device R x m, row-major, float32 or bf16 (ydtype), aligned to its
+ *            element.
+ * 1 <= E <= 1024, 0 <= R, T < 2^31; R = 0 does nothing. Sums are fp32 or better and
+ * in a fixed order: the same inputs give the same y. Products take exact
+ * codes; fp32 x enters as three bf16 parts (all 24 bits). The call is
+ * asynchronous and can be captured into a CUDA graph; ws must then stay the
+ * graph's own. A device-side failure is reported by slim_async_status.
+ * Workspace: slim_dequant_grouped_gemm_workspace_bytes (it may be 0); ws NULL
+ * takes it from the library's pool and returns it in stream order.
+ */
+size_t slim_dequant_grouped_gemm_workspace_bytes(int64_t E, int64_t m, int64_t n, int group, int avg_bits,
+                                                 int xdtype, int64_t R);
+int slim_dequant_grouped_gemm(const uint32_t* codes, const uint8_t* bits, const float* scale,
+                              const float* zero, int64_t E, int64_t m, int64_t n, int group, int avg_bits,
+                              const void* x, int xdtype, int64_t T, const int32_t* row_index,
+                              const int32_t* offsets, int64_t R, void* y, int ydtype, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* The device-side status of the asynchronous calls made on the current device
+ * since the last query: waits for `stream`, returns SLIM_OK or SLIM_ETIMEOUT
+ * (a bounded wait of slim_dequant_grouped_gemm gave up; its y is unspecified)
+ * and clears it. */
+int slim_async_status(void* stream);
+
+/* ------------------------------------------------------------------------
+ * slim_token_logprobs: what a quantized model is judged by and answers with.
+ * Per row of logits, with lse = log sum_v exp(l_v) and p_v = exp(l_v - lse):
+ *   logp     device N float32: l[token] - lse. May be NULL.
+ *   entropy  device N float32: -sum_v p_v log p_v (natural log). May be NULL.
+ *   top_logp, top_id  device N x top_k float32 / int32: the top_k largest
+ *            logits in descending order (equal values: the lower index first),
+ *            as l - lse, and their indices. NULL exactly when top_k = 0.
+ *   logits   device N x V, float32 or bf16 (dtype), rows ld >= V elements
+ *            apart, aligned to the element.
+ *   tokens   device N int64, or NULL. A token outside [0, V) marks a position
+ *            without one (padding): its logp is 0.
+ * 0 <= top_k <= 32, top_k <= V, 1 <= V < 2^31, 0 <= N < 2^31. Logits of
+ * -infinity (masked) have probability 0 and add nothing to the entropy; a row
+ * of nothing else has logp and top_logp -infinity and entropy 0. A NaN or
+ * +infinity makes the row's float outputs NaN (top_id orders NaN above
+ * +infinity). Sums are fp32 in a fixed order. No workspace; the call is
+ * asynchronous and can be captured into a CUDA graph.
+ */
+int slim_token_logprobs(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld,
+                        const int64_t* tokens, int top_k, float* logp, float* entropy, float* top_logp,
+                        int32_t* top_id, void* stream);
+
+/* ------------------------------------------------------------------------
  * slim_quantize_layer: the whole path, hessian -> hinv_diag -> salience ->
  * sba_search -> sqc ([P1] 核心设计: SBA allocates bits between groups, SQC
  * calibrates each group's quantizer), with damping alpha = 0.01.

@@ -620,6 +620,57 @@ def dequant_matmul(words: np.ndarray, bits: Sequence[int], scale: np.ndarray, ze
     return np.asarray(x, dtype=np.float64) @ Wq.T
 
 
+def dequant_grouped_matmul(words: np.ndarray, bits: np.ndarray, scale: np.ndarray, zero: np.ndarray, group: int,
+                           x: np.ndarray, offsets: Sequence[int], row_index=None) -> np.ndarray:
+    """dequant_matmul of several packed layers (experts), each on its rows: grouped row r of expert e,
+    offsets[e] <= r < offsets[e + 1], reads row r of x, or row row_index[r] (zeros when that is outside x).
+    float64 [R, m]; NaN in the rows of no expert."""
+    x = np.asarray(x, dtype=np.float64)
+    R = len(x) if row_index is None else len(row_index)
+    y = np.full((R, np.asarray(scale).shape[1]), np.nan)
+    for e in range(len(offsets) - 1):
+        r0, r1 = (min(max(int(v), 0), R) for v in offsets[e:e + 2])
+        if r1 <= r0:
+            continue
+        if row_index is None:
+            rows = x[r0:r1]
+        else:
+            at = np.asarray(row_index)[r0:r1]
+            inside = (at >= 0) & (at < len(x))
+            rows = np.where(inside[:, None], x[np.where(inside, at, 0)], 0.0)
+        y[r0:r1] = dequant_matmul(words[e], bits[e], scale[e], zero[e], group, rows)
+    return y
+
+
+def token_logprobs(logits: np.ndarray, tokens=None, top_k: int = 0):
+    """(logp, entropy, top_logp, top_id) of rows of logits, float64. -inf logits have probability 0; a row of
+    nothing else has logp and top_logp -inf and entropy 0. A token outside [0, V) gives logp 0. Equal logits
+    rank by index; a NaN ranks above +inf."""
+    l = np.asarray(logits, dtype=np.float64)
+    N, V = l.shape
+    with np.errstate(all="ignore"):
+        top = l.max(axis=1, keepdims=True)
+        base = np.where(np.isneginf(top), 0.0, top)
+        p = np.exp(l - base)
+        total = p.sum(axis=1, keepdims=True)
+        empty = (total == 0.0)[:, 0]
+        log_total = np.where(total == 0.0, 0.0, np.log(total))
+        lp = l - base - log_total
+        lp[np.isnan(total[:, 0])] = np.nan
+        prob = p / total
+        entropy = np.where(empty, 0.0, -np.where(prob == 0.0, 0.0, prob * lp).sum(axis=1))
+    logp = None
+    if tokens is not None:
+        t = np.asarray(tokens)
+        given = (t >= 0) & (t < V)
+        logp = np.where(given, lp[np.arange(N), np.where(given, t, 0)], 0.0)
+    if not top_k:
+        return logp, entropy, None, None
+    rank = np.stack([np.lexsort((np.arange(V), np.where(np.isnan(r), -np.inf, -r), ~np.isnan(r))) for r in l])
+    ids = rank[:, :top_k]
+    return logp, entropy, np.take_along_axis(lp, ids, 1), ids
+
+
 # ---------------------------------------------------------------------------
 # The whole layer
 # ---------------------------------------------------------------------------

@@ -58,6 +58,15 @@ size_t dg_workspace_bytes(int64_t m, int64_t n, int group, int avg_bits, int64_t
 cudaError_t launch_dequant_gemv(const uint32_t* codes, const uint8_t* bits, const float* scale, const float* zero,
                                 int64_t m, int64_t n, int group, int avg_bits, const void* x, int xdtype, int B,
                                 float* y, uint8_t* ws, cudaStream_t s);
+size_t grouped_workspace_bytes(int64_t E, int64_t m, int64_t n, int group, int xdtype, int64_t R);
+cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const float* scale, const float* zero,
+                           int64_t E, int64_t m, int64_t n, int group, int avg_bits, const void* x, int xdtype,
+                           int64_t T, const int32_t* row_index, const int32_t* offsets, int64_t R, void* y,
+                           int ydtype, uint8_t* ws, int num_sms, cudaStream_t s);
+cudaError_t launch_logprobs(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const int64_t* tokens,
+                            int top_k, float* logp, float* entropy, float* top_logp, int32_t* top_id, int num_sms,
+                            cudaStream_t s);
+cudaError_t take_async_status(DevStatus* host, cudaStream_t s);
 cudaError_t launch_gptq(const float* W, int64_t m, int64_t n, const double* H, double alpha, const uint8_t* bits,
                         int group, int avg_bits, double lam, int n_tau, uint32_t* codes, float* scale, float* zero,
                         uint8_t* tau_idx, double* h, double* ws, DevStatus* st, int num_sms, cudaStream_t s);
@@ -121,6 +130,15 @@ int check_shape(int64_t m, int64_t n, int64_t N, int xdtype, int group) {
 }
 
 int check_bits(int avg_bits) { return (avg_bits >= 2 && avg_bits + 1 <= 8) ? SLIM_OK : SLIM_EINVAL; }
+
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int check_grouped(int64_t E, int64_t m, int64_t n, int group, int avg_bits, int xdtype, int64_t R) {
+  if (E < 1 || E > 1024 || R < 0 || R > INT32_MAX) return SLIM_EINVAL;
+  const int rc = check_shape(m, n, 1, xdtype, group);
+  if (rc) return rc;
+  return check_bits(avg_bits);
+}
 
 // Sync the stream, then map CUDA errors and the device status word.
 int finish(cudaStream_t s, const DevStatus* dst) {
@@ -567,6 +585,68 @@ int slim_dequant_gemv(const uint32_t* codes, const uint8_t* bits, const float* s
   rc = w.acquire(ws, ws_bytes, slim_dequant_gemv_workspace_bytes(m, n, group, avg_bits, batch), s);
   if (rc) return rc;
   SLIM_CUDA(launch_dequant_gemv(codes, bits, scale, zero, m, n, group, avg_bits, x, xdtype, (int)batch, y, w.p, s));
+  return SLIM_OK;
+}
+
+size_t slim_dequant_grouped_gemm_workspace_bytes(int64_t E, int64_t m, int64_t n, int group, int avg_bits, int xdtype,
+                                                 int64_t R) {
+  if (check_grouped(E, m, n, group, avg_bits, xdtype, R)) return 0;
+  return grouped_workspace_bytes(E, m, n, group, xdtype, R);
+}
+
+int slim_dequant_grouped_gemm(const uint32_t* codes, const uint8_t* bits, const float* scale, const float* zero,
+                              int64_t E, int64_t m, int64_t n, int group, int avg_bits, const void* x, int xdtype,
+                              int64_t T, const int32_t* row_index, const int32_t* offsets, int64_t R, void* y,
+                              int ydtype, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_grouped(E, m, n, group, avg_bits, xdtype, R);
+  if (rc) return rc;
+  if (T < 0 || T > INT32_MAX || (!row_index && T < R)) return SLIM_EINVAL;
+  if (ydtype != SLIM_X_F32 && ydtype != SLIM_X_BF16) return SLIM_EINVAL;
+  if (R == 0) return SLIM_OK;
+  if (!codes || !bits || !scale || !zero || !x || !offsets || !y || !aligned16(codes) || !aligned16(x) ||
+      !aligned_to(y, ydtype == SLIM_X_F32 ? 4 : 2) || !aligned_to(scale, 4) || !aligned_to(zero, 4) ||
+      !aligned_to(offsets, 4) || !aligned_to(row_index, 4))
+    return SLIM_EINVAL;
+  int sms = 0;
+  rc = device_sms(&sms);
+  if (rc) return rc;
+  if (injected("dequant_grouped_gemm")) return SLIM_EINJECTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Workspace w;
+  w.sync_on_release = false;
+  rc = w.acquire(ws, ws_bytes, grouped_workspace_bytes(E, m, n, group, xdtype, R), s);
+  if (rc) return rc;
+  SLIM_CUDA(launch_grouped(codes, bits, scale, zero, E, m, n, group, avg_bits, x, xdtype, T, row_index, offsets, R, y,
+                           ydtype, w.p, sms, s));
+  return SLIM_OK;
+}
+
+int slim_async_status(void* stream) {
+  int sms = 0;
+  int rc = device_sms(&sms);
+  if (rc) return rc;
+  DevStatus hs;
+  SLIM_CUDA(take_async_status(&hs, static_cast<cudaStream_t>(stream)));
+  g_last_detail = hs.code ? hs.where : 0;
+  return hs.code == 0 ? SLIM_OK : hs.code == kStatusTimeout ? SLIM_ETIMEOUT : SLIM_ECUDA;
+}
+
+int slim_token_logprobs(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const int64_t* tokens,
+                        int top_k, float* logp, float* entropy, float* top_logp, int32_t* top_id, void* stream) {
+  if (dtype != SLIM_X_F32 && dtype != SLIM_X_BF16) return SLIM_EINVAL;
+  if (N < 0 || N > INT32_MAX || V < 1 || V > INT32_MAX || ld < V) return SLIM_EINVAL;
+  if (top_k < 0 || top_k > 32 || top_k > V) return SLIM_EINVAL;
+  if ((top_k > 0) != (top_logp != nullptr) || (top_k > 0) != (top_id != nullptr)) return SLIM_EINVAL;
+  if (N == 0) return SLIM_OK;
+  if (!logits || !aligned_to(logits, dtype == SLIM_X_F32 ? 4 : 2) || !aligned_to(tokens, 8) || !aligned_to(logp, 4) ||
+      !aligned_to(entropy, 4) || !aligned_to(top_logp, 4) || !aligned_to(top_id, 4))
+    return SLIM_EINVAL;
+  int sms = 0;
+  const int rc = device_sms(&sms);
+  if (rc) return rc;
+  if (injected("token_logprobs")) return SLIM_EINJECTED;
+  SLIM_CUDA(launch_logprobs(logits, dtype, N, V, ld, tokens, top_k, logp, entropy, top_logp, top_id, sms,
+                            static_cast<cudaStream_t>(stream)));
   return SLIM_OK;
 }
 

@@ -79,6 +79,11 @@ _SIGS = {
     "slim_gptq": (i32, [vp, i64, i64, vp, vp, i32, i32, dbl, i32, vp, vp, vp, vp, vp, sz, vp]),
     "slim_dequant_gemv_workspace_bytes": (sz, [i64, i64, i32, i32, i64]),
     "slim_dequant_gemv": (i32, [vp, vp, vp, vp, i64, i64, i32, i32, vp, i32, i64, vp, vp, sz, vp]),
+    "slim_dequant_grouped_gemm_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32, i64]),
+    "slim_dequant_grouped_gemm": (i32, [vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, i32, i64, vp, vp, i64, vp, i32,
+                                        vp, sz, vp]),
+    "slim_async_status": (i32, [vp]),
+    "slim_token_logprobs": (i32, [vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp]),
     "slim_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32]),
     "slim_quantize_layer": (i32, [vp, i64, i64, vp, i32, i64, i32, i32, dbl, i32, vp, vp, vp, vp, vp, sz, vp]),
     "slim_quantize_layer_ex": (i32, [vp, i64, i64, vp, i32, i64, i32, i32, dbl, i32, vp, vp, vp, vp, vp, sz, vp,
@@ -321,6 +326,114 @@ def slim_dequant_gemv(codes: torch.Tensor, bits: torch.Tensor, scale: torch.Tens
     _check(_lib().slim_dequant_gemv(_ptr(codes), _ptr(bits), _ptr(scale), _ptr(zero), m, n, group, avg_bits, _ptr(x),
                                     _xdtype(x), B, _ptr(y), _ptr(ws), wsb, _stream(stream)), "slim_dequant_gemv")
     return y
+
+
+_DTYPES = {torch.float32: SLIM_X_F32, torch.bfloat16: SLIM_X_BF16}
+
+
+class _on:
+    """The device of the tensors current, and new tensors allocated for the stream that the call runs on."""
+
+    def __init__(self, device, stream):
+        self.guards = []
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+            self.guards.append(torch.cuda.stream(s))
+        self.device = device
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _need(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def slim_dequant_grouped_gemm(codes: torch.Tensor, bits: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor,
+                              group: int, avg_bits: int, x: torch.Tensor, offsets: torch.Tensor,
+                              row_index: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                              y_dtype: Optional[torch.dtype] = None, ws: Optional[torch.Tensor] = None, stream=None):
+    """Y_e = X_e W_hat_e^T for packed layers codes [E, m, words], bits [E, k], scale and zero [E, m, k];
+    expert e takes the rows offsets[e]..offsets[e + 1] of x [T, n], or with row_index [R] those rows
+    of it. y is [R, m], of y_dtype (x's by default); rows of no expert are left as they are."""
+    E, m, k = scale.shape
+    n = k * group
+    dev = x.device
+    R = x.shape[0] if row_index is None else row_index.shape[0]
+    _need(x.dim() == 2 and x.shape[1] == n and x.dtype in _DTYPES, "x must be [T, n], bf16 or float32")
+    _need(codes.shape == (E, m, n * avg_bits // 32) and codes.dtype in (torch.int32, torch.uint32),
+          "codes must be [E, m, n * avg_bits / 32] int32")
+    _need(bits.shape == (E, k) and bits.dtype == torch.uint8, "bits must be [E, k] uint8")
+    _need(zero.shape == scale.shape and scale.dtype == zero.dtype == torch.float32,
+          "scale and zero must be [E, m, k] float32")
+    _need(offsets.shape == (E + 1,) and offsets.dtype == torch.int32, "offsets must be [E + 1] int32")
+    _need(row_index is None or (row_index.dim() == 1 and row_index.dtype == torch.int32),
+          "row_index must be [R] int32")
+    if y is not None:
+        _need(y.shape == (R, m) and y.dtype in _DTYPES and y_dtype in (None, y.dtype),
+              "y must be [R, m], bf16 or float32")
+    else:
+        y_dtype = x.dtype if y_dtype is None else y_dtype
+        _need(y_dtype in _DTYPES, "y must be [R, m], bf16 or float32")
+    for t in (codes, bits, scale, zero, offsets, row_index, y, ws):
+        _need(t is None or t.device == dev, "all tensors must be on x's device")
+    _need(dev.type == "cuda", "tensors must be on a CUDA device")
+    lib = _lib()
+    with _on(dev, stream) as s:
+        if y is None:
+            y = torch.empty((R, m), dtype=y_dtype, device=dev)
+        if ws is None:
+            wsb = lib.slim_dequant_grouped_gemm_workspace_bytes(E, m, n, group, avg_bits, _DTYPES[x.dtype], R)
+            ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+        else:
+            wsb = ws.numel() * ws.element_size()
+        _check(lib.slim_dequant_grouped_gemm(_ptr(codes), _ptr(bits), _ptr(scale), _ptr(zero), E, m, n, group,
+                                             avg_bits, _ptr(x), _DTYPES[x.dtype], x.shape[0], _ptr(row_index),
+                                             _ptr(offsets), R, _ptr(y), _DTYPES[y.dtype], _ptr(ws), wsb, s),
+               "slim_dequant_grouped_gemm")
+    return y
+
+
+def slim_async_status(stream=None, device=None):
+    """Raises SlimError if an asynchronous call failed on the device since the last query; waits for the stream."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with _on(dev, stream) as s:
+        _check(_lib().slim_async_status(s), "slim_async_status")
+
+
+def slim_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, top_k: int = 0, stream=None):
+    """(logp, entropy, top_logp, top_id) of logits [N, V] (rows may be strided): the log probability of
+    tokens [N] int64 (None without tokens; 0 where a token is outside [0, V)), the entropy, and the
+    top_k largest log probabilities with their indices (None when top_k is 0)."""
+    _need(logits.dim() == 2 and logits.dtype in _DTYPES, "logits must be [N, V], bf16 or float32")
+    N, V = logits.shape
+    dev = logits.device
+    ld = logits.stride(0) if N > 1 else V
+    _need(V >= 1 and (V == 1 or logits.stride(1) == 1) and ld >= V, "the rows of logits must be contiguous")
+    _need(tokens is None or (tokens.shape == (N,) and tokens.dtype == torch.int64 and tokens.device == dev
+                             and tokens.is_contiguous()), "tokens must be [N] int64 on the logits' device")
+    _need(0 <= top_k <= min(32, V), "top_k must be in 0..32 and at most V")
+    _need(dev.type == "cuda", "logits must be on a CUDA device")
+    with _on(dev, stream) as s:
+        logp = None if tokens is None else torch.empty(N, dtype=torch.float32, device=dev)
+        entropy = torch.empty(N, dtype=torch.float32, device=dev)
+        top_logp = top_id = None
+        if top_k:
+            top_logp = torch.empty((N, top_k), dtype=torch.float32, device=dev)
+            top_id = torch.empty((N, top_k), dtype=torch.int32, device=dev)
+        _check(_lib().slim_token_logprobs(logits.data_ptr(), _DTYPES[logits.dtype], N, V, ld, _ptr(tokens), top_k,
+                                          _ptr(logp), _ptr(entropy), _ptr(top_logp), _ptr(top_id), s),
+               "slim_token_logprobs")
+    return logp, entropy, top_logp, top_id
 
 
 # --------------------------------------------------------------------- whole layer
