@@ -337,16 +337,17 @@ int slim_dequant_gemv(const uint32_t* codes, const uint8_t* bits, const float* s
  *            offsets[0], behind offsets[E]) are not written.
  *   y        device R x m, row-major, float32 or bf16 (ydtype), aligned to its
  *            element.
- * 1 <= E <= 1024, 0 <= R, T < 2^31; R = 0 does nothing. Sums are fp32 or better and
+ * 1 <= E <= 1024, E m < 2^31, 0 <= R <= 2^29, 0 <= T < 2^31; R = 0 does nothing. Sums are fp32 or better and
  * in a fixed order: the same inputs give the same y. Products take exact
  * codes; fp32 x enters as three bf16 parts (all 24 bits). The call is
  * asynchronous and can be captured into a CUDA graph; ws must then stay the
  * graph's own. A device-side failure is reported by slim_async_status.
- * Workspace: slim_dequant_grouped_gemm_workspace_bytes (it may be 0); ws NULL
+ * Workspace: slim_dequant_grouped_gemm_workspace_bytes (it may be 0; gathered:
+ * whether row_index is given); ws NULL
  * takes it from the library's pool and returns it in stream order.
  */
 size_t slim_dequant_grouped_gemm_workspace_bytes(int64_t E, int64_t m, int64_t n, int group, int avg_bits,
-                                                 int xdtype, int64_t R);
+                                                 int xdtype, int gathered, int64_t R);
 int slim_dequant_grouped_gemm(const uint32_t* codes, const uint8_t* bits, const float* scale,
                               const float* zero, int64_t E, int64_t m, int64_t n, int group, int avg_bits,
                               const void* x, int xdtype, int64_t T, const int32_t* row_index,

@@ -58,7 +58,7 @@ size_t dg_workspace_bytes(int64_t m, int64_t n, int group, int avg_bits, int64_t
 cudaError_t launch_dequant_gemv(const uint32_t* codes, const uint8_t* bits, const float* scale, const float* zero,
                                 int64_t m, int64_t n, int group, int avg_bits, const void* x, int xdtype, int B,
                                 float* y, uint8_t* ws, cudaStream_t s);
-size_t grouped_workspace_bytes(int64_t E, int64_t m, int64_t n, int group, int xdtype, int64_t R);
+size_t grouped_workspace_bytes(int64_t E, int64_t m, int64_t n, int group, int xdtype, bool gathered, int64_t R);
 cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const float* scale, const float* zero,
                            int64_t E, int64_t m, int64_t n, int group, int avg_bits, const void* x, int xdtype,
                            int64_t T, const int32_t* row_index, const int32_t* offsets, int64_t R, void* y,
@@ -134,9 +134,10 @@ int check_bits(int avg_bits) { return (avg_bits >= 2 && avg_bits + 1 <= 8) ? SLI
 bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int check_grouped(int64_t E, int64_t m, int64_t n, int group, int avg_bits, int xdtype, int64_t R) {
-  if (E < 1 || E > 1024 || R < 0 || R > INT32_MAX) return SLIM_EINVAL;
+  if (E < 1 || E > 1024 || R < 0 || R > (1 << 29)) return SLIM_EINVAL;
   const int rc = check_shape(m, n, 1, xdtype, group);
   if (rc) return rc;
+  if (E * m > INT32_MAX) return SLIM_EINVAL;
   return check_bits(avg_bits);
 }
 
@@ -589,9 +590,9 @@ int slim_dequant_gemv(const uint32_t* codes, const uint8_t* bits, const float* s
 }
 
 size_t slim_dequant_grouped_gemm_workspace_bytes(int64_t E, int64_t m, int64_t n, int group, int avg_bits, int xdtype,
-                                                 int64_t R) {
+                                                 int gathered, int64_t R) {
   if (check_grouped(E, m, n, group, avg_bits, xdtype, R)) return 0;
-  return grouped_workspace_bytes(E, m, n, group, xdtype, R);
+  return grouped_workspace_bytes(E, m, n, group, xdtype, gathered != 0, R);
 }
 
 int slim_dequant_grouped_gemm(const uint32_t* codes, const uint8_t* bits, const float* scale, const float* zero,
@@ -614,7 +615,7 @@ int slim_dequant_grouped_gemm(const uint32_t* codes, const uint8_t* bits, const 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Workspace w;
   w.sync_on_release = false;
-  rc = w.acquire(ws, ws_bytes, grouped_workspace_bytes(E, m, n, group, xdtype, R), s);
+  rc = w.acquire(ws, ws_bytes, grouped_workspace_bytes(E, m, n, group, xdtype, row_index != nullptr, R), s);
   if (rc) return rc;
   SLIM_CUDA(launch_grouped(codes, bits, scale, zero, E, m, n, group, avg_bits, x, xdtype, T, row_index, offsets, R, y,
                            ydtype, w.p, sms, s));

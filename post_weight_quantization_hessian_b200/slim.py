@@ -79,7 +79,7 @@ _SIGS = {
     "slim_gptq": (i32, [vp, i64, i64, vp, vp, i32, i32, dbl, i32, vp, vp, vp, vp, vp, sz, vp]),
     "slim_dequant_gemv_workspace_bytes": (sz, [i64, i64, i32, i32, i64]),
     "slim_dequant_gemv": (i32, [vp, vp, vp, vp, i64, i64, i32, i32, vp, i32, i64, vp, vp, sz, vp]),
-    "slim_dequant_grouped_gemm_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32, i64]),
+    "slim_dequant_grouped_gemm_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32, i32, i64]),
     "slim_dequant_grouped_gemm": (i32, [vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, i32, i64, vp, vp, i64, vp, i32,
                                         vp, sz, vp]),
     "slim_async_status": (i32, [vp]),
@@ -392,7 +392,8 @@ def slim_dequant_grouped_gemm(codes: torch.Tensor, bits: torch.Tensor, scale: to
         if y is None:
             y = torch.empty((R, m), dtype=y_dtype, device=dev)
         if ws is None:
-            wsb = lib.slim_dequant_grouped_gemm_workspace_bytes(E, m, n, group, avg_bits, _DTYPES[x.dtype], R)
+            wsb = lib.slim_dequant_grouped_gemm_workspace_bytes(E, m, n, group, avg_bits, _DTYPES[x.dtype],
+                                                                row_index is not None, R)
             ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
         else:
             wsb = ws.numel() * ws.element_size()

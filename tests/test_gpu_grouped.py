@@ -254,7 +254,7 @@ def test_another_stream_and_a_caller_workspace(R):
     want = slim.slim_dequant_grouped_gemm(*dev, 128, 2, x, off)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
-    need = slim._lib().slim_dequant_grouped_gemm_workspace_bytes(1, m, n, 128, 2, 0, R)
+    need = slim._lib().slim_dequant_grouped_gemm_workspace_bytes(1, m, n, 128, 2, 0, 0, R)
     ws = torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     y1 = slim.slim_dequant_grouped_gemm(*dev, 128, 2, x, off, stream=s)

@@ -32,7 +32,8 @@ def grouped(lib, **kw):
     (dict(avg=1), "avg_bits below 2"),
     (dict(avg=8), "avg_bits above 7"),
     (dict(R=-1), "negative row count"),
-    (dict(R=2 ** 31), "row count past 31 bits"),
+    (dict(R=2 ** 29 + 1, T=2 ** 30), "too many rows"),
+    (dict(E=1024, m=2 ** 21), "E m past 31 bits"),
     (dict(T=99), "fewer rows of x than grouped rows, and no index"),
     (dict(T=-1, index=0x8000), "negative T"),
     (dict(xd=2), "unknown x dtype"),
@@ -57,8 +58,8 @@ def test_grouped_refusals(lib, kw, why):
 
 def test_grouped_of_no_rows_is_ok_without_a_device(lib):
     assert grouped(lib, R=0, T=0) == 0
-    assert lib.slim_dequant_grouped_gemm_workspace_bytes(4, 256, 640, 128, 2, 1, 0) == 0
-    assert lib.slim_dequant_grouped_gemm_workspace_bytes(4, 256, 641, 128, 2, 1, 100) == 0   # not a valid call
+    assert lib.slim_dequant_grouped_gemm_workspace_bytes(4, 256, 641, 128, 2, 1, 1, 100) == 0
+    assert lib.slim_dequant_grouped_gemm_workspace_bytes(4, 256, 640, 96, 2, 1, 0, 100) == 0   # not a valid call
 
 
 @pytest.mark.parametrize("kw, why", [
