@@ -130,21 +130,174 @@ gg_prep_kernel(const void* __restrict__ x, int xdtype, int64_t T, const int32_t*
   }
 }
 
-// ---------------------------------------------------------------- tensor cores
+// ---------------------------------------------------------------- many rows
+// Experts with more than kFewRows rows: their codes are decoded once into bf16
+// tiles in the workspace (gd_kernel), and a tensor-core kernel (gg_tc_kernel)
+// multiplies the tiles with x. The tiles of one pass over the outputs are kept
+// small enough for L2.
+// (A kernel that decoded each tile inside the product loop was built first: 265 us
+// on 4096 rows of a 4096 x 4096 layer, bound by the decoding warps and the
+// barriers between the roles, a wait of 150 cycles each; every 256 rows decoded
+// the layer again.)
+constexpr int GT_M = 128, GT_N = 256, GT_K = 64;
+constexpr int GT_MAX_E = 1024;
+constexpr int GT_ABYTES = GT_M * GT_K * 2, GT_XBYTES = GT_N * GT_K * 2;
+
+struct GtParams {
+  const uint32_t* codes;
+  const uint8_t* bits;
+  const float* scale;
+  const float* zero;
+  const int32_t* offsets;
+  uint8_t* tiles;  // [slot][output tile of the pass][box] of 16 KB
+  void* y;
+  int64_t m, n, R, rw;
+  int E, k, planes, few_rows, max_slots;
+  int mt0, mtn;    // output tiles of this pass: first, count
+};
+struct GtMaps {
+  CUtensorMap x256, x32, s256, s32;
+};
+
+__device__ __forceinline__ int gt_clamp(int v, int64_t R) { return max(0, min(v, (int)R)); }
+
+// The slots of the experts with more than few_rows rows, in order: s_expert[slot].
+// At most max_slots of them, which offsets that do not descend never exceed. One warp.
+__device__ __forceinline__ int gt_slots(const GtParams& p, int lane, int* s_expert) {
+  int run = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 32) {
+    const int e = e0 + lane;
+    const bool many =
+        e < p.E && gt_clamp(p.offsets[e + 1], p.R) - gt_clamp(p.offsets[e], p.R) > p.few_rows;
+    const unsigned mask = __ballot_sync(0xffffffffu, many);
+    if (many) s_expert[run + __popc(mask & ((1u << lane) - 1))] = e;
+    run += __popc(mask);
+  }
+  return min(run, p.max_slots);
+}
+
+// ---------------------------------------------------------------- decoding
+// One block: 128 outputs x up to 16 boxes of 64 columns of one slot. A thread
+// takes 8 codes (b bytes of the row's stream) and writes the 16 bytes of their
+// bf16 values where the product's shared-memory layout wants them (K-major, 128-
+// byte swizzle), so that a warp writes 512 consecutive bytes and the product
+// loads a whole tile with one bulk copy. Behind the boxes of codes come those of
+// the correction columns. Bound by the bytes written.
+constexpr int GD_THREADS = 256, GD_BOXES = 16;
+
+template <int B, bool kCenter>
+__device__ __forceinline__ uint4 decode8(uint32_t lo, uint32_t hi) {
+  uint32_t w[B], o[16];
+#pragma unroll
+  for (int q = 0; q < B; ++q) w[q] = q == 0 ? lo : (q == 1 ? hi : 0u);
+  decode32<B, kCenter>(w, o);  // (only the first 8 codes are kept: the rest is dropped at compile time)
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int G, bool kCenter>
+__global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
+  constexpr int kSlots = kCenter ? 8 : 4, kUnits = G / 32, kCorr = GT_K / kSlots;
+  __shared__ int s_expert[GT_MAX_E];
+  __shared__ int s_count, s_before;
+  __shared__ uint32_t s_width[GD_BOXES * 2];  // first word << 4 | width, of each 32-column unit
+  const int tid = threadIdx.x, lane = tid & 31, slot = blockIdx.z;
+  if (tid == 0) s_before = 0;
+  if (tid < 32) {
+    const int c = gt_slots(p, lane, s_expert);
+    if (lane == 0) s_count = c;
+  }
+  __syncthreads();
+  if (slot >= s_count) return;
+  const int e = s_expert[slot], nbox = (int)((p.n + GT_K - 1) / GT_K), ncor = (p.k + kCorr - 1) / kCorr;
+  const int kb0 = blockIdx.x * GD_BOXES, kb1 = min(kb0 + GD_BOXES, nbox + ncor);
+  const uint8_t* bits = p.bits + (int64_t)e * p.k;
+  const int64_t m0 = (int64_t)(p.mt0 + blockIdx.y) * GT_M;
+  uint8_t* out = p.tiles + ((int64_t)slot * p.mtn + blockIdx.y) * (nbox + ncor) * GT_ABYTES;
+  // widths before the block's boxes, then the block's own
+  int before = 0;
+  const int c0 = kb0 * 2 / kUnits;
+  for (int c = tid; c < min(c0, p.k); c += GD_THREADS) before += bits[c] <= 8 ? bits[c] : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  if (lane == 0) atomicAdd(&s_before, before);  // (integers: the order does not matter)
+  __syncthreads();
+  if (tid < 32) {  // lane = unit of the block
+    const int unit = kb0 * 2 + lane, c = unit / kUnits;
+    int b = c < p.k ? bits[c] : 0;
+    if (b > 8) b = 0;
+    int incl = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int first = s_before * kUnits + incl - b;
+    // widths that do not fill a row: nothing outside it is read
+    s_width[lane] = first + b > p.rw ? 0u : (uint32_t)first << 4 | (uint32_t)b;
+  }
+  __syncthreads();
+  const int chunk = tid & 7, h = chunk >> 2;
+  for (int kb = kb0; kb < kb1; ++kb) {
+    const bool cor = kb >= nbox;
+    uint8_t* tile = out + (int64_t)kb * GT_ABYTES;
+    const uint32_t en = s_width[(kb - kb0) * 2 + h], b = en & 15, first = en >> 4;
+#pragma unroll 4
+    for (int row = tid >> 3; row < GT_M; row += GD_THREADS / 8) {
+      const int64_t i = (int64_t)e * p.m + min(m0 + row, p.m - 1);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (!cor) {
+        const uint32_t bit = (chunk & 3) * 8 * b, sh = bit & 31;
+        const uint32_t* w = p.codes + i * p.rw + first + (bit >> 5);
+        uint32_t lo = 0, hi = 0;
+        if (b) {  // 8 b bits from bit `sh` on: never past the unit's b words
+          const uint32_t w0 = __ldg(w), w1 = sh + 8 * b > 32 ? __ldg(w + 1) : 0u;
+          lo = __funnelshift_r(w0, w1, sh);
+          if (b > 4) hi = sh + 8 * b > 64 ? __funnelshift_r(w1, __ldg(w + 2), sh) : w1 >> sh;
+        }
+        switch (b) {
+          case 1: v = decode8<1, kCenter>(lo, hi); break;
+          case 2: v = decode8<2, kCenter>(lo, hi); break;
+          case 3: v = decode8<3, kCenter>(lo, hi); break;
+          case 4: v = decode8<4, kCenter>(lo, hi); break;
+          case 5: v = decode8<5, kCenter>(lo, hi); break;
+          case 6: v = decode8<6, kCenter>(lo, hi); break;
+          case 7: v = decode8<7, kCenter>(lo, hi); break;
+          case 8: v = decode8<8, kCenter>(lo, hi); break;
+          default: break;
+        }
+      } else {
+        uint32_t o[4];
+#pragma unroll
+        for (int z = 0; z < 8 / kSlots; ++z) {
+          const int c = (kb - nbox) * kCorr + chunk * (8 / kSlots) + z, bc = c < p.k ? bits[c] : 0;
+          const float cx =
+              bc >= 1 && bc <= 8 ? coef_x<kCenter>(bc, p.scale[i * p.k + c], p.zero[i * p.k + c]) : 0.f;
+          uint32_t part[kSlots / 2];
+          split_slots<kSlots, true>(cx, part);
+#pragma unroll
+          for (int y = 0; y < kSlots / 2; ++y) o[z * (kSlots / 2) + y] = part[y];
+        }
+        v = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      *reinterpret_cast<uint4*>(tile + row * 128 + ((chunk ^ (row & 7)) << 4)) = v;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- product
 // A persistent CTA per SM takes tiles of 128 outputs x up to 256 rows (an
-// expert's rows cut evenly, in multiples of 16, so that a narrow remainder does
-// not cost a tile's decoding). The whole depth n is one tile's; per 64 columns
-// (a box):
-//   warps 8..15  decode the 128 x 64 codes into the A operand in shared memory
-//                (thread = output row; K-major, 128-byte swizzle), two sets of four
-//                warps on alternate boxes
-//   warp 16      x boxes (64 columns x rows) by TMA, the B operand
-//   warp 17      tcgen05.mma M=128 x N=rows x K=16, A x B^T into tensor memory:
+// expert's rows cut evenly, in multiples of 16). The whole depth is one tile's;
+// per box of 64 columns:
+//   warp 8       the decoded 128 x 64 tile (one bulk copy) and the x box (TMA)
+//   warp 9       tcgen05.mma M=128 x N=rows x K=16, A x B^T into tensor memory:
 //                each group into its own accumulator, two in flight
-//   warp 18      windows of 16 code words x 128 rows by TMA
-//   warps 0..7   per group: acc += coef_d D in packed fp32 pairs, thread = output
-//                row, two warps a row set on alternate 32 columns; at the end y
-//                (a warp stores 32 consecutive outputs of a row)
+//   warp 10      the gate: arrives on a box's barrier, beside the copies, once the
+//                accumulator that the box starts is free. So the issuing warp has
+//                one wait a box (a wait is 150 cycles even when nothing is left
+//                to wait for; a box's products take 512 at 256 rows)
+//   warps 0..7   per group: acc += coef_d D in packed fp32 pairs, thread = output,
+//                two warps an output set on alternate 32 rows; at the end y (a
+//                warp stores 32 consecutive outputs of a row)
 // The other term, sum over groups of coef_x xs, is a product of its own of depth
 // k: its factors are fp32, so each is cut into bf16 parts and the products of the
 // parts stand side by side as correction columns (4 a group for a bf16 y, 8 for
@@ -153,36 +306,17 @@ gg_prep_kernel(const void* __restrict__ x, int xdtype, int64_t T, const int32_t*
 // bounds groups of 64 and 32.
 // Rows of two neighbouring experts may share an x box: an accumulator column
 // depends on its own row of x alone, and only the tile's rows are stored.
-constexpr int GT_M = 128, GT_N = 256, GT_K = 64;
-constexpr int GT_THREADS = 640;
-constexpr int GT_XS = 4, GT_AS = 3, GT_CS = 4;  // ring lengths: x, A, code windows
-constexpr int GT_XBYTES = GT_N * GT_K * 2, GT_ABYTES = GT_M * GT_K * 2;
-constexpr int GT_WIN = 16, GT_CBYTES = GT_M * GT_WIN * 4;
-constexpr int GT_OFF_A = GT_XS * GT_XBYTES;
-constexpr int GT_OFF_C = GT_OFF_A + GT_AS * GT_ABYTES;
-constexpr int GT_OFF_BAR = GT_OFF_C + GT_CS * GT_CBYTES;
-constexpr int GT_OFF_E = GT_OFF_BAR + 512;
-constexpr int GT_MAX_E = 1024;
-constexpr int GT_SMEM = GT_OFF_E + 2 * (GT_MAX_E + 1) * 4 + 1024;  // + alignment
+constexpr int GT_THREADS = 384;
+constexpr int GT_STAGES = 4;
+constexpr int GT_STAGE = GT_ABYTES + GT_XBYTES;
+constexpr int GT_OFF_BAR = GT_STAGES * GT_STAGE;
+constexpr int GT_OFF_E = GT_OFF_BAR + 256;
+constexpr int GT_SMEM = GT_OFF_E + (2 * GT_MAX_E + 1) * 4 + 1024;  // + alignment
 static_assert(GT_SMEM <= 227 * 1024, "shared memory of a CTA");
 
-struct GtParams {
-  const uint32_t* codes;
-  const uint8_t* bits;
-  const float* scale;
-  const float* zero;
-  const int32_t* offsets;
-  void* y;
-  int64_t m, n, R, rw;
-  int E, k, planes, ydtype, codes_tma, mtiles;
-};
-struct GtMaps {
-  CUtensorMap x256, x32, s256, s32, codes;
-};
-
 struct GtTile {
-  int e;        // expert
-  int64_t m0;   // first output
+  int e, slot;  // expert and its slot
+  int mt;       // output tile of the pass
   int col0;     // first row of x
   int r1;       // end of the expert's rows
   int N;        // accumulator columns
@@ -216,12 +350,17 @@ __device__ __forceinline__ uint64_t gt_fma2(uint64_t a, uint64_t b, uint64_t c) 
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // Bounded wait. A poll suspends the warp in hardware for up to 20 us, so that
 // waiting warps take no issue slots from the working ones; the limit on polls
 // (a healthy phase completes in microseconds) turns a would-be hang into a
-// recorded failure. Kept small: it is inlined at every wait, and the roles'
-// loops have to stay in the instruction cache together (with a clock and a
-// second loop in it the kernel was 289 KB of code and ran 3 to 4 times slower).
+// recorded failure. (%globaltimer is not read here: that costs more than a phase.)
 constexpr int kWaitPolls = 100000;
 __device__ __forceinline__ bool gt_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int where) {
 #pragma unroll 1
@@ -241,107 +380,101 @@ __device__ __forceinline__ bool gt_wait(uint32_t bar, uint32_t parity, volatile 
 
 // Tiles of the rows [r0, r1): count, and the width of each.
 __device__ __forceinline__ int gt_row_tiles(int r0, int r1, int& width) {
-  if (r1 <= r0) {
-    width = 0;
-    return 0;
-  }
   const int span = r1 - r0, nt = (span + GT_N - 1) / GT_N;
-  width = ((span + nt - 1) / nt + 15) & ~15;
+  width = nt ? ((span + nt - 1) / nt + 15) & ~15 : 0;
   return nt;
 }
 
-__device__ __forceinline__ GtTile gt_tile(const GtParams& p, int t, const int* first, const int* off) {
-  int lo = 0, hi = p.E;  // the last expert whose first tile is <= t
+// first[s]: the row tiles of the slots before s, times the output tiles of the pass.
+__device__ __forceinline__ GtTile gt_tile(const GtParams& p, int t, int slots, const int* first, const int* expert) {
+  int lo = 0, hi = slots;  // the last slot whose first tile is <= t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (first[mid] <= t) lo = mid; else hi = mid;
   }
   GtTile u;
-  u.e = lo;
-  u.r1 = off[lo + 1];
+  u.slot = lo;
+  u.e = expert[lo];
+  const int r0 = gt_clamp(p.offsets[u.e], p.R);
+  u.r1 = gt_clamp(p.offsets[u.e + 1], p.R);
   int width;
-  gt_row_tiles(off[lo], u.r1, width);
-  const int j = (t - first[lo]) / p.mtiles;
-  u.m0 = (int64_t)(t - first[lo] - j * p.mtiles) * GT_M;
-  u.col0 = off[lo] + j * width;
+  gt_row_tiles(r0, u.r1, width);
+  const int j = (t - first[lo]) / p.mtn;
+  u.mt = t - first[lo] - j * p.mtn;
+  u.col0 = r0 + j * width;
   u.N = (min(width, u.r1 - u.col0) + 15) & ~15;
   return u;
 }
 
 template <int G, bool kCenter>
 __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_constant__ GtMaps tm, const GtParams p) {
-  constexpr int kSlots = kCenter ? 8 : 4;       // correction columns of a group
-  constexpr int kUnits = G / 32;                // 32-code units of a group
-  constexpr int kCorr = GT_K / kSlots;          // groups of a correction box
+  constexpr int kCorr = GT_K / (kCenter ? 8 : 4);  // groups of a correction box
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sx = smem;
-  uint8_t* sa = smem + GT_OFF_A;
-  uint8_t* sc = smem + GT_OFF_C;
-  uint64_t* xfull = reinterpret_cast<uint64_t*>(smem + GT_OFF_BAR);
-  uint64_t* xempty = xfull + GT_XS;
-  uint64_t* afull = xempty + GT_XS;
-  uint64_t* aempty = afull + GT_AS;
-  uint64_t* cfull = aempty + GT_AS;
-  uint64_t* cempty = cfull + GT_CS;
-  uint64_t* dfull = cempty + GT_CS;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + GT_OFF_BAR);
+  uint64_t* empty = full + GT_STAGES;
+  uint64_t* dfull = empty + GT_STAGES;
   uint64_t* dempty = dfull + 2;
   uint64_t* done = dempty + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  int* s_slots = reinterpret_cast<int*>(tslot + 2);
   int* s_first = reinterpret_cast<int*>(smem + GT_OFF_E);
-  int* s_off = s_first + GT_MAX_E + 1;
+  int* s_expert = s_first + GT_MAX_E + 1;
 
   const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: roles' loops run on uniform registers
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: the roles' loops run on uniform registers
   if (tid == 0) {
-    for (int i = 0; i < GT_XS; ++i) { mbar_init(&xfull[i], 1); mbar_init(&xempty[i], 1); }
-    for (int i = 0; i < GT_AS; ++i) { mbar_init(&afull[i], 4); mbar_init(&aempty[i], 1); }
-    for (int i = 0; i < GT_CS; ++i) { mbar_init(&cfull[i], 1); mbar_init(&cempty[i], 8); }
+    for (int i = 0; i < GT_STAGES; ++i) { mbar_init(&full[i], 2); mbar_init(&empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&dfull[i], 1); mbar_init(&dempty[i], 8); }
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm.x256);
     tma_prefetch_desc(&tm.x32);
-    if (p.codes_tma) tma_prefetch_desc(&tm.codes);
   }
-  if (warp == 19) tmem_alloc(tslot, 512);
-  for (int e = tid; e <= p.E; e += GT_THREADS) s_off[e] = max(0, min(p.offsets[e], (int)p.R));
-  __syncthreads();
-  if (warp == 0) {  // tiles before each expert
+  if (warp == 11) tmem_alloc(tslot, 512);
+  if (warp == 0) {  // slots and the tiles before each
+    const int slots = gt_slots(p, lane, s_expert);
+    __syncwarp();
     int run = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane;
+    for (int q0 = 0; q0 < slots; q0 += 32) {
+      const int q = q0 + lane;
       int width, v = 0;
-      if (e < p.E) v = gt_row_tiles(s_off[e], s_off[e + 1], width) * p.mtiles;
+      if (q < slots) {
+        const int e = s_expert[q];
+        v = gt_row_tiles(gt_clamp(p.offsets[e], p.R), gt_clamp(p.offsets[e + 1], p.R), width) * p.mtn;
+      }
       int incl = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += u;
       }
-      if (e < p.E) s_first[e] = run + incl - v;
+      if (q < slots) s_first[q] = run + incl - v;
       run += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) s_first[p.E] = run;
+    if (lane == 0) {
+      s_first[slots] = run;
+      *s_slots = slots;
+    }
   }
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tslot;
-  const int tiles = s_first[p.E];
+  const int slots = *s_slots, tiles = s_first[slots];
   const int nbox = (int)((p.n + GT_K - 1) / GT_K);     // boxes of codes
   const int ncor = (p.k + kCorr - 1) / kCorr;          // boxes of correction columns
 
   if (warp < 8) {
     // ------------------------------------------------------------ epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int half = warp >> 2, sub = (warp & 3) * 32;
     GtRing dr;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const GtTile u = gt_tile(p, t, s_first, s_off);
-      const int64_t i = u.m0 + sub + lane;
+      const GtTile u = gt_tile(p, t, slots, s_first, s_expert);
+      const int64_t i = (int64_t)(p.mt0 + u.mt) * GT_M + sub + lane;
       const bool row_ok = i < p.m;
       const float* scale = p.scale + ((int64_t)u.e * p.m + (row_ok ? i : p.m - 1)) * p.k;
       const uint8_t* bits = p.bits + (int64_t)u.e * p.k;
@@ -368,7 +501,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
           if (c + 1 < p.k) bnext = bits[c + 1];
         }
         const uint64_t cd2 = gt_pack(cd, cd);
-        if (!gt_wait(smem_u32(dfull) + 8 * (dr.slot), dr.phase, abort_flag, 11)) {
+        if (!gt_wait(smem_u32(dfull) + 8 * dr.slot, dr.phase, abort_flag, 11)) {
           ok = false;
           break;
         }
@@ -378,16 +511,12 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
         for (int q = 0; q < 4; ++q) {
           const int col = (2 * q + half) * 32;
           if (col < u.N) {
+            uint32_t d[32];
+            tmem_ld32(dcol + col, d);
+            tc_wait_ld();
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              uint32_t d[16];
-              tmem_ld16(dcol + col + 16 * w, d);
-              tc_wait_ld16(d);
-#pragma unroll
-              for (int v = 0; v < 8; ++v)
-                acc[q * 16 + w * 8 + v] =
-                    gt_fma2(cd2, ((uint64_t)d[2 * v + 1] << 32) | d[2 * v], acc[q * 16 + w * 8 + v]);
-            }
+            for (int v = 0; v < 16; ++v)
+              acc[q * 16 + v] = gt_fma2(cd2, ((uint64_t)d[2 * v + 1] << 32) | d[2 * v], acc[q * 16 + v]);
           }
         }
         tc_fence_before();
@@ -421,315 +550,195 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
         yp += 64 * p.m;
       }
     }
-  } else if (warp < 16) {
-    // ------------------------------------------------------------ decoding
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    const int row = tid & 127, set = (warp - 8) >> 2;  // the two sets of four warps take alternate boxes
-    uint32_t ai = 0;  // boxes of all tiles so far
-    uint32_t ci = 0;  // windows taken so far
-    bool ok = true;
-    const int nwin = (int)((p.rw + GT_WIN - 1) / GT_WIN), rw = (int)p.rw;
-    const uint32_t cbase = smem_u32(sc) + row * (GT_WIN * 4), cswz = ((row >> 1) & 3) << 4;
-    const uint32_t abase = smem_u32(sa) + row * 128, aswz = (row & 7) << 4;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const GtTile u = gt_tile(p, t, s_first, s_off);
-      const uint8_t* bits = p.bits + (int64_t)u.e * p.k;
-      const int64_t i = (int64_t)u.e * p.m + (u.m0 + row < p.m ? u.m0 + row : p.m - 1);
-      const uint32_t* crow = p.codes + i * p.rw;
-      int wpos = 0, have = 0, freed = 0;  // words and windows of this tile: read, arrived, given back
-      const uint32_t cslot = ci;  // ring position of the tile's window 0
-      // (a set takes the windows of the boxes it leaves to the other set too, so that no warp gives a
-      // window back a second time before every warp has given it back once)
-      auto take_windows = [&](int upto) {
-#pragma unroll 1
-        for (; p.codes_tma && have < upto && ok; ++have, ++ci)
-          ok = gt_wait(smem_u32(cfull) + 8 * (ci % GT_CS), (ci / GT_CS) & 1, abort_flag, 20);
-      };
-      auto free_windows = [&](int upto) {
-#pragma unroll 1
-        for (; p.codes_tma && freed < upto && ok; ++freed) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&cempty[(cslot + freed) % GT_CS]);
-        }
-      };
-      auto begin_box = [&]() {
-        if (ok) ok = gt_wait(smem_u32(aempty) + 8 * (ai % GT_AS), ((ai / GT_AS) & 1) ^ 1, abort_flag, 21);
-        return abase + (ai % GT_AS) * GT_ABYTES;
-      };
-      auto end_box = [&]() {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&afull[ai % GT_AS]);
-      };
-      auto store16 = [&](uint32_t to, int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((chunk * 16) ^ aswz)), "r"(a), "r"(b),
-                     "r"(c), "r"(d)
-                     : "memory");
-      };
-      uint32_t bcache = 0;
-#pragma unroll 1
-      for (int kb = 0; kb < nbox && ok; ++kb, ++ai) {
-        // the widths of the box's two units, and the words before and of them
-        int b[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = (2 * kb + h) / kUnits;
-          if ((2 * kb + h) % (32 * kUnits) == 0) bcache = c + lane < p.k ? bits[c + lane] : 0;
-          b[h] = __shfl_sync(0xffffffffu, bcache, c & 31);
-          if (kUnits > 1 && h == 0) b[1] = b[0];
-          if (kUnits > 1) break;
-        }
-        if (b[0] > 8 || wpos + b[0] > rw) b[0] = 0;  // not a width: nothing of this group counts
-        if (b[1] > 8 || wpos + b[0] + b[1] > rw) b[1] = 0;
-        const int wend = wpos + b[0] + b[1];
-        take_windows((wend + GT_WIN - 1) / GT_WIN);
-        if ((kb & 1) == set) {
-          uint32_t to = 0;
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint32_t o[16];
-            switch (b[h]) {
-#define GT_CASE(B)                                                                                  \
-  case B: {                                                                                         \
-    uint32_t w[B];                                                                                  \
-    _Pragma("unroll") for (int q = 0; q < B; ++q) {                                                 \
-      const uint32_t wi = (uint32_t)(wpos + q);                                                     \
-      if (p.codes_tma)                                                                              \
-        asm volatile("ld.shared.u32 %0, [%1];"                                                      \
-                     : "=r"(w[q])                                                                   \
-                     : "r"(cbase + ((cslot + wi / GT_WIN) % GT_CS) * GT_CBYTES +                    \
-                           (((wi % GT_WIN) * 4) ^ cswz)));                                          \
-      else /* rows that are not 16-byte aligned */                                                  \
-        w[q] = __ldg(crow + wi);                                                                    \
-    }                                                                                               \
-    decode32<B, kCenter>(w, o);                                                                     \
-  } break;
-              GT_CASE(1) GT_CASE(2) GT_CASE(3) GT_CASE(4) GT_CASE(5) GT_CASE(6) GT_CASE(7) GT_CASE(8)
-#undef GT_CASE
-              default:
-#pragma unroll
-                for (int q = 0; q < 16; ++q) o[q] = 0u;
-            }
-            if (h == 0) to = begin_box();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) store16(to, h * 4 + q, o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-            wpos += b[h];
-          }
-          end_box();
-        }
-        wpos = wend;
-        free_windows(wpos / GT_WIN);
-      }
-      take_windows(nwin);
-      free_windows(nwin);
-      // the correction columns: coef_x of each group in bf16 parts
-      const float* sc_row = p.scale + i * p.k;
-      const float* ze_row = p.zero + i * p.k;
-#pragma unroll 1
-      for (int q = 0; q < ncor && ok; ++q, ++ai) {
-        if ((q & 1) != set) continue;
-        const uint32_t to = begin_box();
-#pragma unroll 1
-        for (int v = 0; v < kCorr; v += 8) {  // 8 groups' scales and zeros in flight at a time
-          float sv[8], zv[8];
-#pragma unroll
-          for (int w = 0; w < 8; ++w) {
-            const int c = min(q * kCorr + v + w, p.k - 1);
-            sv[w] = sc_row[c];
-            zv[w] = ze_row[c];
-          }
-#pragma unroll
-          for (int w = 0; w < 8; w += 8 / kSlots) {  // a 16-byte chunk
-            uint32_t o[4];
-#pragma unroll
-            for (int z = 0; z < 8 / kSlots; ++z) {
-              const int c = q * kCorr + v + w + z;
-              const int b = c < p.k ? bits[c] : 0;
-              const float cx = b >= 1 && b <= 8 ? coef_x<kCenter>(b, sv[w + z], zv[w + z]) : 0.f;
-              uint32_t part[kSlots / 2];
-              split_slots<kSlots, true>(cx, part);
-#pragma unroll
-              for (int y = 0; y < kSlots / 2; ++y) o[z * (kSlots / 2) + y] = part[y];
-            }
-            store16(to, (v + w) * kSlots / 8, o[0], o[1], o[2], o[3]);
-          }
-        }
-        end_box();
-      }
-    }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-    if (warp == 16 && lane == 0) {
-      // ---------------------------------------------------------- x boxes
-      uint32_t xi = 0;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8 && lane == 0) {
+      // ---------------------------------------------------------- copies
+      GtRing r;
+      uint32_t issued = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const GtTile u = gt_tile(p, t, s_first, s_off);
-        const int per = u.N > 128 ? 1 : (u.N > 64 ? 2 : 4);  // boxes of a stage
-        for (int kb = 0; kb < nbox + ncor && ok;) {
+        const GtTile u = gt_tile(p, t, slots, s_first, s_expert);
+        const uint8_t* at = p.tiles + ((int64_t)u.slot * p.mtn + u.mt) * (nbox + ncor) * GT_ABYTES;
+        const int nr = (u.N + 31) / 32;
+        const uint32_t bytes = (u.N > 128 ? GT_XBYTES : nr * 4096) + GT_ABYTES;
+        for (int kb = 0; kb < nbox + ncor && ok; ++kb) {
           const bool cor = kb >= nbox;
-          const int k0 = cor ? kb - nbox : kb, nb = min(per, (cor ? nbox + ncor : nbox) - kb);
-          for (int pl = cor ? 0 : p.planes - 1; pl >= 0; --pl, ++xi) {
-            const uint32_t s = xi % GT_XS;
-            if (!gt_wait(smem_u32(xempty) + 8 * (s), ((xi / GT_XS) & 1) ^ 1, abort_flag, 30)) {
+          // fp32 x: a stage for every plane, the small parts first, each with the decoded tile
+          for (int pl = cor ? 0 : p.planes - 1; pl >= 0; --pl, ++issued) {
+            if (!gt_wait(smem_u32(empty) + 8 * r.slot, r.phase ^ 1, abort_flag, 30)) {
               ok = false;
               break;
             }
-            const int y0 = (int)(pl * p.R) + u.col0;
-            uint8_t* dst = sx + s * GT_XBYTES;
-            if (per == 1) {
-              mbar_arrive_expect_tx(&xfull[s], GT_XBYTES);
-              tma_load_2d(dst, cor ? &tm.s256 : &tm.x256, &xfull[s], k0 * GT_K, y0);
+            uint8_t* dst = smem + r.slot * GT_STAGE;
+            uint64_t* bar = &full[r.slot];
+            mbar_arrive_expect_tx(bar, bytes);
+            bulk_load(dst, at + (int64_t)kb * GT_ABYTES, GT_ABYTES, bar);
+            const int x0 = (cor ? kb - nbox : kb) * GT_K, y0 = (int)(pl * p.R) + u.col0;
+            dst += GT_ABYTES;
+            if (u.N > 128) {
+              tma_load_2d(dst, cor ? &tm.s256 : &tm.x256, bar, x0, y0);
             } else {
-              const int nr = (u.N + 31) / 32;
-              mbar_arrive_expect_tx(&xfull[s], (uint32_t)(nb * nr * 4096));
-              for (int q = 0; q < nb; ++q)
-                for (int v = 0; v < nr; ++v)
-                  tma_load_2d(dst + q * (GT_XBYTES / per) + v * 4096, cor ? &tm.s32 : &tm.x32, &xfull[s],
-                              (k0 + q) * GT_K, y0 + 32 * v);
+              for (int v = 0; v < nr; ++v) tma_load_2d(dst + v * 4096, cor ? &tm.s32 : &tm.x32, bar, x0, y0 + 32 * v);
             }
+            r.step(GT_STAGES);
           }
-          kb += nb;
         }
       }
-      for (uint32_t j = xi > GT_XS ? xi - GT_XS : 0; j < xi; ++j) mbar_drain(&xfull[j % GT_XS], (j / GT_XS) & 1);
-    } else if (warp == 17) {
+      // let every issued copy land before the CTA can exit, also after an abort
+      for (uint32_t j = issued > GT_STAGES ? issued - GT_STAGES : 0; ok == false && j < issued; ++j)
+        mbar_drain(&full[j % GT_STAGES], (j / GT_STAGES) & 1);
+    } else if (warp == 10 && lane == 0) {
+      // ---------------------------------------------------------- gate
+      GtRing r, dr;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int kb = 0; kb < nbox + ncor && ok; ++kb) {
+          const bool cor = kb >= nbox;
+          // accumulators that the box starts (groups of 32: both of its halves)
+          const int starts = cor ? kb == nbox : (G == 128 ? (kb & 1) == 0 : (G == 64 ? 1 : min(2, p.k - 2 * kb)));
+          const int planes = cor ? 1 : p.planes;
+          for (int q = 0; q < planes && ok; ++q) {
+            // its arrival has to fall into the stage's current use
+            ok = gt_wait(smem_u32(empty) + 8 * r.slot, r.phase ^ 1, abort_flag, 31);
+            if (q == 0 && G != 32)
+              for (int v = 0; v < starts && ok; ++v) {
+                ok = gt_wait(smem_u32(dempty) + 8 * dr.slot, dr.phase ^ 1, abort_flag, 32);
+                dr.step(2);
+              }
+            if (ok) mbar_arrive(&full[r.slot]);
+            r.step(GT_STAGES);
+          }
+        }
+      }
+    } else if (warp == 9) {
       // ---------------------------------------------------------- matrix products
       // The whole warp runs the loop (uniform control and registers); one elected
       // lane issues. What stands between two products is kept to a few instructions.
       const bool lead = elect_one();
       constexpr uint64_t kDesc = ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
                                  ((uint64_t)2 << 61);  // K-major, 128-byte swizzle (sdesc_sw128)
-      const uint32_t a0 = smem_u32(sa) >> 4, x0 = smem_u32(sx) >> 4;
-      GtRing xr, ar, dr;
+      const uint32_t a0 = smem_u32(smem) >> 4;
+      GtRing r, dr;
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const GtTile u = gt_tile(p, t, s_first, s_off);
-        const int per = u.N > 128 ? 1 : (u.N > 64 ? 2 : 4);
-        const uint32_t xstep = (GT_XBYTES / 16) / per;
+        const GtTile u = gt_tile(p, t, slots, s_first, s_expert);
         const uint32_t idesc = idesc_bf16_f32(GT_M, 16, false, false) + ((uint32_t)(u.N / 8 - 2) << 17);
-        int sub = 0;
-        // kSteps products of 16 columns from every plane; fresh: the first of an accumulator
-        auto part = [&](auto steps, uint32_t koff, int planes, uint32_t fresh, bool wait_x, bool free_x) {
-          constexpr int kSteps = decltype(steps)::value;
-          const uint64_t ad = kDesc + (a0 + ar.slot * (GT_ABYTES / 16) + koff);
-          const uint32_t d = tbase + dr.slot * GT_N;
-          uint32_t slot = xr.slot, phase = xr.phase, acc = fresh ^ 1u;
-#pragma unroll 1
-          for (int q = 0; q < planes; ++q) {
-            if (wait_x) {
-              if (!gt_wait(smem_u32(xfull) + 8 * slot, phase, abort_flag, 42)) return false;
-              tc_fence_after();
-            }
-            const uint64_t bd = kDesc + (x0 + slot * (GT_XBYTES / 16) + sub * xstep + koff);
-            if (lead) {
-#pragma unroll
-              for (int k16 = 0; k16 < kSteps; ++k16) tc_mma_bf16(d, ad + 2 * k16, bd + 2 * k16, idesc, k16 ? 1u : acc);
-              if (free_x) tc_commit(&xempty[slot]);
-            }
-            acc = 1u;
-            if (++slot == GT_XS) {
-              slot = 0;
-              phase ^= 1;
-            }
-          }
-          if (free_x) {
-            xr.slot = slot;
-            xr.phase = phase;
-          }
-          return true;
-        };
-        // boxes [0, n) of codes (kParts parts each, begins and ends of groups known) or of correction columns
-        auto boxes = [&](auto parts, auto per_group, int n, int planes, bool odd) {
-          constexpr int kParts = decltype(parts)::value, kPer = decltype(per_group)::value;
+        // kPer: boxes of a group (0: all n boxes are one); kParts: groups of a box
+        auto boxes = [&](auto per_group, int n, int planes) {
+          constexpr int kPer = decltype(per_group)::value;
 #pragma unroll 1
           for (int kb = 0; kb < n; ++kb) {
-            if (!gt_wait(smem_u32(afull) + 8 * ar.slot, ar.phase, abort_flag, 40)) return false;
-            const bool last = kb == n - 1, last_sub = sub == per - 1 || last;
             const bool begins = kPer == 0 ? kb == 0 : (kPer == 1 || (kb & 1) == 0);
-            const bool ends = kPer == 0 ? last : (kPer == 1 || (kb & 1) == 1);
-#pragma unroll
-            for (int h = 0; h < kParts; ++h) {
-              const bool only = kParts == 1 || (last && odd);
-              if (h == 1 && only) break;
-              if (begins && !gt_wait(smem_u32(dempty) + 8 * dr.slot, dr.phase ^ 1, abort_flag, 41)) return false;
+            const bool ends = kPer == 0 ? kb == n - 1 : (kPer == 1 || (kb & 1) == 1);
+#pragma unroll 1
+            for (int q = 0; q < planes; ++q) {
+              if (!gt_wait(smem_u32(full) + 8 * r.slot, r.phase, abort_flag, 40)) return false;
               tc_fence_after();
-              if (!part(std::integral_constant<int, 4 / kParts>{}, (uint32_t)h * 4, planes, begins,
-                        sub == 0 && h == 0, last_sub && (h == 1 || only)))
-                return false;
-              if (ends) {
-                if (lead) tc_commit(&dfull[dr.slot]);
-                dr.step(2);
+              const uint64_t ad = kDesc + (a0 + r.slot * (GT_STAGE / 16)), bd = ad + GT_ABYTES / 16;
+              if (lead) {
+#pragma unroll
+                for (int k16 = 0; k16 < 4; ++k16)
+                  tc_mma_bf16(tbase + dr.slot * GT_N, ad + 2 * k16, bd + 2 * k16, idesc,
+                              k16 == 0 && q == 0 && begins ? 0u : 1u);
+                tc_commit(&empty[r.slot]);
+                if (ends && q == planes - 1) tc_commit(&dfull[dr.slot]);
               }
+              r.step(GT_STAGES);
             }
-            sub = last_sub ? 0 : sub + 1;
-            if (lead) tc_commit(&aempty[ar.slot]);
-            ar.step(GT_AS);
+            if (ends) dr.step(2);
           }
           return true;
         };
-        ok = boxes(std::integral_constant<int, G == 32 ? 2 : 1>{}, std::integral_constant<int, G == 128 ? 2 : 1>{}, nbox,
-                   p.planes, (p.k & 1) != 0) &&
-             boxes(std::integral_constant<int, 1>{}, std::integral_constant<int, 0>{}, ncor, 1, false);
+        // groups of 32: a box's two groups in turn, each from every plane; a stage is
+        // given back after the second, so the planes of a box are all held at once
+        auto boxes32 = [&](int n, int planes) {
+#pragma unroll 1
+          for (int kb = 0; kb < n; ++kb) {
+            const int parts = min(2, p.k - 2 * kb);
+            GtRing rs = r;
+#pragma unroll 1
+            for (int h = 0; h < parts; ++h) {
+              if (!gt_wait(smem_u32(dempty) + 8 * dr.slot, dr.phase ^ 1, abort_flag, 41)) return false;
+              rs = r;
+#pragma unroll 1
+              for (int q = 0; q < planes; ++q) {
+                if (h == 0 && !gt_wait(smem_u32(full) + 8 * rs.slot, rs.phase, abort_flag, 42)) return false;
+                tc_fence_after();
+                const uint64_t ad = kDesc + (a0 + rs.slot * (GT_STAGE / 16) + 4 * h), bd = ad + GT_ABYTES / 16;
+                if (lead) {
+                  tc_mma_bf16(tbase + dr.slot * GT_N, ad, bd, idesc, q == 0 ? 0u : 1u);
+                  tc_mma_bf16(tbase + dr.slot * GT_N, ad + 2, bd + 2, idesc, 1u);
+                  if (h == parts - 1) tc_commit(&empty[rs.slot]);
+                }
+                rs.step(GT_STAGES);
+              }
+              if (lead) tc_commit(&dfull[dr.slot]);
+              dr.step(2);
+            }
+            r = rs;
+          }
+          return true;
+        };
+        if constexpr (G == 32) {
+          ok = boxes32(nbox, p.planes);
+          if (ok) ok = gt_wait(smem_u32(dempty) + 8 * dr.slot, dr.phase ^ 1, abort_flag, 41);
+        } else {
+          ok = boxes(std::integral_constant<int, G == 128 ? 2 : 1>{}, nbox, p.planes);
+        }
+        if (ok) ok = boxes(std::integral_constant<int, 0>{}, ncor, 1);
       }
       // every issued product completes before tensor memory can be freed, also after an abort
       if (lead) {
         tc_commit(done);
         mbar_drain(done, 0);
       }
-    } else if (warp == 18 && lane == 0 && p.codes_tma) {
-      // ---------------------------------------------------------- code windows
-      uint32_t ci = 0;
-      bool ok = true;
-      const int nwin = (int)((p.rw + GT_WIN - 1) / GT_WIN);
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const GtTile u = gt_tile(p, t, s_first, s_off);
-        const int y0 = (int)(u.e * p.m + u.m0);
-        for (int w = 0; w < nwin; ++w, ++ci) {
-          const uint32_t s = ci % GT_CS;
-          if (!gt_wait(smem_u32(cempty) + 8 * (s), ((ci / GT_CS) & 1) ^ 1, abort_flag, 50)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&cfull[s], GT_CBYTES);
-          tma_load_2d(sc + s * GT_CBYTES, &tm.codes, &cfull[s], w * GT_WIN, y0);
-        }
-      }
-      for (uint32_t j = ci > GT_CS ? ci - GT_CS : 0; j < ci; ++j) mbar_drain(&cfull[j % GT_CS], (j / GT_CS) & 1);
     }
     __syncwarp();
   }
   __syncthreads();
   if (tid == 0 && *abort_flag) record_failure(&g_async_status, kStatusTimeout, *abort_flag);
-  if (warp == 19) {
+  if (warp == 11) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
 }
 
 // ---------------------------------------------------------------- host side
+constexpr int kFewRows = 0;  // experts with at most this many rows are left to the few-rows kernel
+constexpr size_t kTileBytes = size_t(64) << 20;  // decoded tiles of a pass: they stay in L2 (126 MB)
+
 struct GroupedPlan {
-  int planes;         // bf16 planes copied in grouped order (0: x is read as it is)
-  int64_t xs_stride;  // correction columns of a row, padded to 16 bytes
-  size_t off_xg, bytes;
+  int planes;          // bf16 planes copied in grouped order (0: x is read as it is)
+  int64_t xs_stride;   // correction columns of a row
+  int64_t slots;       // experts that can have many rows
+  int64_t mtiles, mt;  // output tiles in all and of a pass
+  size_t off_xg, off_tiles, bytes;
 };
 
 // For an fp32 y the correction columns are 8 a group; the plan has room for either.
-static GroupedPlan grouped_plan(int64_t n, int group, int xdtype, bool gathered, int64_t R) {
+static GroupedPlan grouped_plan(int64_t E, int64_t m, int64_t n, int group, int xdtype, bool gathered, int64_t R) {
   GroupedPlan g{};
-  g.xs_stride = n / group * 8;
+  const int64_t k = n / group, boxes = (n + GT_K - 1) / GT_K + (k + 7) / 8;
+  g.xs_stride = k * 8;
   g.planes = xdtype == 0 ? 3 : (gathered ? 1 : 0);
+  g.slots = std::min<int64_t>(E, R / (kFewRows + 1));
+  g.mtiles = (m + GT_M - 1) / GT_M;
+  const size_t each = (size_t)std::max<int64_t>(g.slots, 1) * boxes * GT_ABYTES;  // one output tile of every slot
+  g.mt = std::min<int64_t>(g.mtiles, std::max<int64_t>(1, (int64_t)(kTileBytes / each)));
+  if (g.slots == 0) return g;
   g.off_xg = ((size_t)R * g.xs_stride * 2 + 255) & ~size_t(255);
-  g.bytes = g.off_xg + (((size_t)g.planes * R * n * 2 + 255) & ~size_t(255));
+  g.off_tiles = g.off_xg + (((size_t)g.planes * R * n * 2 + 255) & ~size_t(255));
+  g.bytes = g.off_tiles + each * g.mt;
   return g;
 }
 
 size_t grouped_workspace_bytes(int64_t E, int64_t m, int64_t n, int group, int xdtype, bool gathered, int64_t R) {
-  return grouped_plan(n, group, xdtype, gathered, R).bytes;
+  return grouped_plan(E, m, n, group, xdtype, gathered, R).bytes;
 }
 
 template <int G, bool kCenter>
-static cudaError_t launch_gt(const GtMaps& tm, const GtParams& p, int num_sms, cudaStream_t s) {
+static cudaError_t launch_many(const GtMaps& tm, GtParams p, const GroupedPlan& g, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> attr{0};
   uint64_t bit = 0;
   if (attr_pending(attr, bit)) {
@@ -738,8 +747,15 @@ static cudaError_t launch_gt(const GtMaps& tm, const GtParams& p, int num_sms, c
     if (e != cudaSuccess) return e;
     attr.fetch_or(bit);
   }
-  gg_tc_kernel<G, kCenter><<<num_sms, GT_THREADS, GT_SMEM, s>>>(tm, p);
-  count_launches(1);
+  constexpr int kCorr = GT_K / (kCenter ? 8 : 4);
+  const int boxes = (int)((p.n + GT_K - 1) / GT_K) + (p.k + kCorr - 1) / kCorr;
+  for (int64_t mt = 0; mt < g.mtiles; mt += g.mt) {
+    p.mt0 = (int)mt;
+    p.mtn = (int)std::min<int64_t>(g.mt, g.mtiles - mt);
+    gd_kernel<G, kCenter><<<dim3((boxes + GD_BOXES - 1) / GD_BOXES, p.mtn, (unsigned)g.slots), GD_THREADS, 0, s>>>(p);
+    gg_tc_kernel<G, kCenter><<<num_sms, GT_THREADS, GT_SMEM, s>>>(tm, p);
+    count_launches(2);
+  }
   return cudaGetLastError();
 }
 
@@ -747,7 +763,7 @@ cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const flo
                            int64_t E, int64_t m, int64_t n, int group, int avg_bits, const void* x, int xdtype,
                            int64_t T, const int32_t* row_index, const int32_t* offsets, int64_t R, void* y,
                            int ydtype, uint8_t* ws, int num_sms, cudaStream_t s) {
-  const GroupedPlan g = grouped_plan(n, group, xdtype, row_index != nullptr, R);
+  const GroupedPlan g = grouped_plan(E, m, n, group, xdtype, row_index != nullptr, R);
   uint16_t* xs = reinterpret_cast<uint16_t*>(ws);
   uint16_t* xg = g.planes ? reinterpret_cast<uint16_t*>(ws + g.off_xg) : nullptr;
   const int k = (int)(n / group);
@@ -762,21 +778,20 @@ cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const flo
   if (e != cudaSuccess) return e;
   GtParams p{};
   p.codes = codes; p.bits = bits; p.scale = scale; p.zero = zero; p.offsets = offsets; p.y = y;
+  p.tiles = ws + g.off_tiles;
   p.m = m; p.n = n; p.R = R; p.rw = n * avg_bits / 32;
-  p.E = (int)E; p.k = k; p.planes = g.planes ? g.planes : 1; p.ydtype = ydtype;
-  p.mtiles = (int)((m + GT_M - 1) / GT_M);
-  p.codes_tma = p.rw % 4 == 0;
+  p.E = (int)E; p.k = k; p.planes = g.planes ? g.planes : 1; p.few_rows = kFewRows;
+  p.max_slots = (int)g.slots;
   GtMaps tm;
   const void* xb = xg ? static_cast<const void*>(xg) : x;
   const uint64_t rows = xg ? (uint64_t)g.planes * R : (uint64_t)T;
+  const uint64_t xs_bytes = (uint64_t)g.xs_stride * 2;
   if (!make_tmap_bf16(&tm.x256, xb, (uint64_t)n, rows, GT_K, GT_N) ||
       !make_tmap_bf16(&tm.x32, xb, (uint64_t)n, rows, GT_K, 32) ||
-      !make_tmap_2byte_strided(&tm.s256, xs, (uint64_t)k * slots, (uint64_t)R, (uint64_t)g.xs_stride * 2, GT_K, GT_N) ||
-      !make_tmap_2byte_strided(&tm.s32, xs, (uint64_t)k * slots, (uint64_t)R, (uint64_t)g.xs_stride * 2, GT_K, 32))
+      !make_tmap_2byte_strided(&tm.s256, xs, (uint64_t)k * slots, (uint64_t)R, xs_bytes, GT_K, GT_N) ||
+      !make_tmap_2byte_strided(&tm.s32, xs, (uint64_t)k * slots, (uint64_t)R, xs_bytes, GT_K, 32))
     return cudaErrorInvalidValue;
-  if (p.codes_tma && !make_tmap_u32_sw64(&tm.codes, codes, (uint64_t)p.rw, (uint64_t)(E * m), GT_WIN, GT_M))
-    return cudaErrorInvalidValue;
-#define SLIM_GT(G) (ydtype == 0 ? launch_gt<G, true>(tm, p, num_sms, s) : launch_gt<G, false>(tm, p, num_sms, s))
+#define SLIM_GT(G) (ydtype == 0 ? launch_many<G, true>(tm, p, g, num_sms, s) : launch_many<G, false>(tm, p, g, num_sms, s))
   return group == 32 ? SLIM_GT(32) : (group == 64 ? SLIM_GT(64) : SLIM_GT(128));
 #undef SLIM_GT
 }
