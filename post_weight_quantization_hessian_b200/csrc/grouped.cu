@@ -104,7 +104,7 @@ gg_prep_kernel(const void* __restrict__ x, int xdtype, int64_t T, const int32_t*
     float s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     for (int o = 1; o < per; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (j >= n) continue;
-    if (lane % per == 0) {
+    if (xs && lane % per == 0) {
       uint32_t o[kSlots / 2];
       split_slots<kSlots, false>(s, o);
       uint16_t* dst = xs + r * xs_stride + j / group * kSlots;
@@ -704,8 +704,327 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
   }
 }
 
+// ---------------------------------------------------------------- few rows
+// Experts with at most few_rows rows (single tokens, small batches): every
+// packed byte is read once and decoded into registers as the A fragments of
+// mma.m16n8k16, whose two other operands of a k-step (rows of x) come from shared
+// memory. What bounds it is the decoding (about 1.3 integer operations a code)
+// next to HBM, not the tensor work, so the warp-level instruction fits: no
+// operand passes through shared or tensor memory.
+//
+// A CTA of 4 warps takes 128 outputs (a warp 32) and a range of 256-column
+// chunks; the CTAs of a cluster share the outputs and split the depth, and add
+// their sums through distributed shared memory in a fixed order. Codes and x
+// arrive by asynchronous copies, two chunks ahead; scales and zeros go through
+// registers one chunk ahead. In a 32-column unit thread (g, t) of a warp takes
+// the 8 codes 8 t .. 8 t + 7 of rows g, g + 8, g + 16, g + 24: as k-steps may
+// take the columns in any order that x follows, those are its four pairs of two
+// k-steps, and x's are 16 consecutive bytes. The group sums of x are the product
+// with a row of ones.
+constexpr int GS_THREADS = 128, GS_M = 128, GS_K = 256, GS_STAGES = 3;
+constexpr int GS_XSTRIDE = GS_K * 2 + 64;  // bytes of a row of x: eight rows' 16-byte reads meet no bank twice
+
+struct GsParams {
+  const uint32_t* codes;
+  const uint8_t* bits;
+  const float* scale;
+  const float* zero;
+  const void* x;             // bf16, [planes][rows][n]
+  const int32_t* row_index;  // of x, or null
+  const int32_t* offsets;
+  void* y;
+  int64_t m, n, R, rw, plane;  // plane: values between two planes of x
+  int64_t T;
+  int E, k, ydtype, few_rows, mtiles, split;
+  int cap, wstride;          // code words of a row in a stage, and their stride
+};
+
+__device__ __forceinline__ void gs_cp16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void gs_cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void gs_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// kNT: tiles of 8 rows at a time; kPlanes: bf16 planes of x.
+template <int G, bool kCenter, int kNT, int kPlanes>
+__global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
+  constexpr int kUnits = G / 32, kGroups = GS_K / G, kRows = 8 * kNT;
+  extern __shared__ __align__(16) uint8_t gs_smem[];
+  __shared__ int s_expert, s_found;
+  __shared__ uint32_t s_width[1024];               // first word << 4 | width of each group
+  __shared__ float2 s_coef[2][kGroups][GS_M];      // coef_d, coef_x
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  const int rank = blockIdx.x % p.split, mt = blockIdx.x / p.split;
+  // the expert of this slot among those with 1 .. few_rows rows
+  if (warp == 0) {
+    int run = 0, mine = -1;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int rows = e < p.E ? gt_clamp(p.offsets[e + 1], p.R) - gt_clamp(p.offsets[e], p.R) : 0;
+      const unsigned mask = __ballot_sync(0xffffffffu, rows > 0 && rows <= p.few_rows);
+      const int at = (int)blockIdx.y - run;
+      if (mine < 0 && at >= 0 && at < __popc(mask)) mine = e0 + (int)__fns(mask, 0, at + 1);
+      run += __popc(mask);
+    }
+    if (lane == 0) {
+      s_expert = mine;
+      s_found = mine >= 0;
+    }
+  }
+  __syncthreads();
+  if (!s_found) return;  // (the same for every CTA of a cluster)
+  const int e = s_expert, r0 = gt_clamp(p.offsets[e], p.R), r1 = gt_clamp(p.offsets[e + 1], p.R);
+  if (warp == 0) {
+    const uint8_t* bits = p.bits + (int64_t)e * p.k;
+    int run = 0;
+#pragma unroll 4
+    for (int c0 = 0; c0 < p.k; c0 += 32) {
+      const int c = c0 + lane;
+      int b = c < p.k ? bits[c] : 0;
+      if (b > 8) b = 0;
+      int incl = b;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const int first = (run + incl - b) * kUnits;
+      if (first + b * kUnits > p.rw) b = 0;  // widths that do not fill a row: nothing outside it is read
+      if (c < p.k) s_width[c] = (uint32_t)(first << 4 | b);
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  __syncthreads();
+  const int chunks = (int)((p.n + GS_K - 1) / GS_K);
+  const int ch0 = chunks * rank / p.split, ch1 = chunks * (rank + 1) / p.split;
+  const int64_t m0 = (int64_t)mt * GS_M, base = (int64_t)e * p.m;
+  const int mrows = (int)min((int64_t)GS_M, p.m - m0);
+  const uint32_t sbase = smem_u32(gs_smem);
+  const uint32_t xbytes = kPlanes * kRows * GS_XSTRIDE, stage = xbytes + GS_M * p.wstride * 4;
+  const bool wide = (p.rw & 3) == 0;  // rows of 16-byte multiples
+  const int64_t srow = (base + m0 + min(tid, mrows - 1)) * p.k;  // this thread's scales and zeros
+
+  // words [first, end) of a chunk
+  auto chunk_words = [&](int ch, int& first, int& end) {
+    const int c0 = ch * kGroups, c1 = min(c0 + kGroups, p.k) - 1;
+    first = (int)(s_width[c0] >> 4);
+    end = (int)(s_width[c1] >> 4) + (int)(s_width[c1] & 15) * kUnits;
+    first = min(first, (int)p.rw);
+    end = min(end, (int)p.rw);
+    if (wide) first &= ~3;
+  };
+  for (int q0 = r0; q0 < r1; q0 += kRows) {
+    const int rows = min(kRows, r1 - q0), nt = (rows + 7) / 8;
+    float acc[2][kNT][4];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int b = 0; b < kNT; ++b)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[a][b][c] = 0.f;
+    auto copy_chunk = [&](int ch, int slot) {
+      if (ch < ch1) {
+        const uint32_t sx = sbase + slot * stage, sw = sx + xbytes;
+        const int cols = (int)min((int64_t)GS_K, p.n - (int64_t)ch * GS_K);
+        for (int v = tid; v < kPlanes * nt * 8 * 32; v += GS_THREADS) {
+          const int c = v & 31, r = v >> 5, pl = kPlanes > 1 ? r / (nt * 8) : 0, rr = kPlanes > 1 ? r - pl * (nt * 8) : r;
+          int64_t src = q0 + rr;
+          bool have = rr < rows && c * 8 < cols;
+          if (have && p.row_index) {
+            src = p.row_index[src];
+            have = src >= 0 && src < p.T;
+          }
+          if (!have) src = 0;
+          gs_cp16(sx + (pl * kRows + rr) * GS_XSTRIDE + c * 16,
+                  static_cast<const uint16_t*>(p.x) + pl * p.plane + src * p.n + (have ? ch * GS_K + c * 8 : 0),
+                  have ? 16u : 0u);  // 0: zeros
+        }
+        int first, end;
+        chunk_words(ch, first, end);
+        end = min(end, first + p.cap);
+        const uint32_t* src = p.codes + (base + m0) * p.rw;
+        if (wide) {
+          for (int r = tid >> 3; r < mrows; r += GS_THREADS / 8)
+            for (int w = first + (tid & 7) * 4; w < end; w += 32)
+              gs_cp16(sw + (r * p.wstride + w - first) * 4, src + (int64_t)r * p.rw + w, 16u);
+        } else {
+          for (int r = tid >> 3; r < mrows; r += GS_THREADS / 8)
+            for (int w = first + (tid & 7); w < end; w += 8)
+              gs_cp4(sw + (r * p.wstride + w - first) * 4, src + (int64_t)r * p.rw + w);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float sreg[kGroups], zreg[kGroups];
+    auto load_scales = [&](int ch) {
+#pragma unroll
+      for (int c = 0; c < kGroups; ++c) {
+        const int at = min(ch * kGroups + c, p.k - 1);
+        sreg[c] = __ldg(p.scale + srow + at);
+        zreg[c] = __ldg(p.zero + srow + at);
+      }
+    };
+    copy_chunk(ch0, 0);
+    copy_chunk(ch0 + 1, 1);
+    if (ch0 < ch1) load_scales(ch0);
+    int slot = 0;
+    for (int ch = ch0; ch < ch1; ++ch) {
+      // coefficients of this chunk (their buffer was last read two chunks ago)
+#pragma unroll
+      for (int c = 0; c < kGroups; ++c) {
+        const int at = ch * kGroups + c, b = at < p.k ? s_width[at] & 15 : 0;
+        s_coef[ch & 1][c][tid] = b ? make_float2(coef_d<kCenter>(b, sreg[c]), coef_x<kCenter>(b, sreg[c], zreg[c]))
+                                   : make_float2(0.f, 0.f);
+      }
+      if (ch + 1 < ch1) load_scales(ch + 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncthreads();  // this chunk has arrived for all; the slot of the last one is free
+      copy_chunk(ch + 2, slot == 0 ? 2 : slot - 1);
+      int first, end;
+      chunk_words(ch, first, end);
+      const uint32_t sx = sbase + slot * stage + g * GS_XSTRIDE + t4 * 16;
+      const uint32_t sw = sbase + slot * stage + xbytes + (warp * 32 + g) * p.wstride * 4;
+      const bool fits = end - first <= p.cap;
+#pragma unroll 1
+      for (int c = 0; c < kGroups; ++c) {
+        if (ch * kGroups + c >= p.k) break;
+        const uint32_t en = s_width[ch * kGroups + c], b = en & 15;
+        if (b == 0) continue;  // not a width
+        float d[2][kNT][4], xs[kNT][4];
+#pragma unroll
+        for (int q = 0; q < kNT; ++q)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) d[0][q][v] = d[1][q][v] = xs[q][v] = 0.f;
+        const int wrel = (int)(en >> 4) - first;
+#pragma unroll 1
+        for (int u = 0; u < kUnits; ++u) {
+          // 8 codes (b bytes) of four rows
+          const uint32_t bit = (uint32_t)(wrel + u * b) * 32 + t4 * 8 * b, sh = bit & 31;
+          uint32_t lo[4], hi[4], A[4][4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            uint32_t w0, w1 = 0, w2 = 0;
+            if (fits) {
+              const uint32_t at = sw + r * 8 * p.wstride * 4 + (bit >> 5) * 4;
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(at));
+              if (b == 3 || b > 4) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w1) : "r"(at + 4));
+              if (b > 4) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w2) : "r"(at + 8));
+            } else {  // wider than the stage was made for: straight from global memory
+              const int row = min(warp * 32 + g + 8 * r, mrows - 1);
+              const uint32_t* src = p.codes + (base + m0 + row) * p.rw;
+              const int64_t w = first + (bit >> 5);
+              w0 = w < p.rw ? __ldg(src + w) : 0u;
+              w1 = w + 1 < p.rw ? __ldg(src + w + 1) : 0u;
+              w2 = w + 2 < p.rw ? __ldg(src + w + 2) : 0u;
+            }
+            lo[r] = __funnelshift_r(w0, w1, sh);
+            hi[r] = __funnelshift_r(w1, w2, sh);
+          }
+          switch (b) {
+#define GS_CASE(B)                                                      \
+  case B:                                                               \
+    _Pragma("unroll") for (int r = 0; r < 4; ++r) {                     \
+      const uint4 v = decode8<B, kCenter>(lo[r], hi[r]);                \
+      A[r][0] = v.x; A[r][1] = v.y; A[r][2] = v.z; A[r][3] = v.w;       \
+    }                                                                   \
+    break;
+            GS_CASE(1) GS_CASE(2) GS_CASE(3) GS_CASE(4) GS_CASE(5) GS_CASE(6) GS_CASE(7) GS_CASE(8)
+#undef GS_CASE
+            default:
+#pragma unroll
+              for (int r = 0; r < 4; ++r) A[r][0] = A[r][1] = A[r][2] = A[r][3] = 0u;
+          }
+          const uint32_t xu = sx + (c * kUnits + u) * 64;
+#pragma unroll
+          for (int pl = kPlanes - 1; pl >= 0; --pl)
+#pragma unroll
+            for (int q = 0; q < kNT; ++q)
+              if (q < nt) {
+                uint32_t b0, b1, b2, b3;
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
+                             : "r"(xu + (pl * kRows + q * 8) * GS_XSTRIDE));
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                  gs_mma(d[a][q], A[2 * a][0], A[2 * a + 1][0], A[2 * a][1], A[2 * a + 1][1], b0, b1);
+                  gs_mma(d[a][q], A[2 * a][2], A[2 * a + 1][2], A[2 * a][3], A[2 * a + 1][3], b2, b3);
+                }
+                gs_mma(xs[q], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, b0, b1);
+                gs_mma(xs[q], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, b2, b3);
+              }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float2 co = s_coef[ch & 1][c][warp * 32 + g + 8 * r];
+#pragma unroll
+          for (int q = 0; q < kNT; ++q)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              float& to = acc[r >> 1][q][(r & 1) * 2 + v];
+              to = fmaf(co.x, d[r >> 1][q][(r & 1) * 2 + v], fmaf(co.y, xs[q][v], to));
+            }
+        }
+      }
+      slot = slot == 2 ? 0 : slot + 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    // the CTA's sums [row of x][output], then the cluster's in rank order
+    float* red = reinterpret_cast<float*>(gs_smem);
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int q = 0; q < kNT; ++q)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (q < nt) red[(q * 8 + t4 * 2 + (v & 1)) * GS_M + warp * 32 + a * 16 + g + (v >> 1) * 8] = acc[a][q][v];
+    if (p.split > 1) {
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+      __syncthreads();
+    }
+    for (int v = tid + rank * GS_THREADS; v < rows * GS_M; v += GS_THREADS * p.split) {
+      const int r = v / GS_M, o = v % GS_M;
+      if (o >= mrows) continue;
+      float sum = 0.f;
+      for (int z = 0; z < p.split; ++z) {
+        float f;
+        if (p.split > 1) {
+          uint32_t at;
+          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(sbase + v * 4), "r"(z));
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(at) : "memory");
+        } else {
+          f = red[v];
+        }
+        sum += f;
+      }
+      const int64_t to = (int64_t)(q0 + r) * p.m + m0 + o;
+      if constexpr (kCenter)
+        static_cast<float*>(p.y)[to] = sum;
+      else
+        static_cast<uint16_t*>(p.y)[to] = (uint16_t)pack_bf16(sum, 0.f);
+    }
+    if (p.split > 1) {
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+      __syncthreads();
+    }
+  }
+}
+
 // ---------------------------------------------------------------- host side
-constexpr int kFewRows = 0;  // experts with at most this many rows are left to the few-rows kernel
+constexpr int kFewRows = 32;  // experts with at most this many rows: the few-rows kernel
 constexpr size_t kTileBytes = size_t(64) << 20;  // decoded tiles of a pass: they stay in L2 (126 MB)
 
 struct GroupedPlan {
@@ -720,16 +1039,18 @@ struct GroupedPlan {
 static GroupedPlan grouped_plan(int64_t E, int64_t m, int64_t n, int group, int xdtype, bool gathered, int64_t R) {
   GroupedPlan g{};
   const int64_t k = n / group, boxes = (n + GT_K - 1) / GT_K + (k + 7) / 8;
-  g.xs_stride = k * 8;
-  g.planes = xdtype == 0 ? 3 : (gathered ? 1 : 0);
   g.slots = std::min<int64_t>(E, R / (kFewRows + 1));
   g.mtiles = (m + GT_M - 1) / GT_M;
-  const size_t each = (size_t)std::max<int64_t>(g.slots, 1) * boxes * GT_ABYTES;  // one output tile of every slot
-  g.mt = std::min<int64_t>(g.mtiles, std::max<int64_t>(1, (int64_t)(kTileBytes / each)));
-  if (g.slots == 0) return g;
-  g.off_xg = ((size_t)R * g.xs_stride * 2 + 255) & ~size_t(255);
+  g.planes = xdtype == 0 ? 3 : (gathered && g.slots ? 1 : 0);
+  g.xs_stride = k * 8;
+  if (g.slots) {
+    const size_t each = (size_t)g.slots * boxes * GT_ABYTES;  // one output tile of every slot
+    g.mt = std::min<int64_t>(g.mtiles, std::max<int64_t>(1, (int64_t)(kTileBytes / each)));
+    g.off_xg = ((size_t)R * g.xs_stride * 2 + 255) & ~size_t(255);
+    g.bytes = each * g.mt;
+  }
   g.off_tiles = g.off_xg + (((size_t)g.planes * R * n * 2 + 255) & ~size_t(255));
-  g.bytes = g.off_tiles + each * g.mt;
+  g.bytes += g.off_tiles;
   return g;
 }
 
@@ -759,29 +1080,96 @@ static cudaError_t launch_many(const GtMaps& tm, GtParams p, const GroupedPlan& 
   return cudaGetLastError();
 }
 
+template <int G, bool kCenter, int kNT, int kPlanes>
+static cudaError_t launch_few(GsParams p, int64_t slots, int avg_bits, int num_sms, cudaStream_t s) {
+  static std::atomic<uint64_t> attr{0};
+  uint64_t bit = 0;
+  if (attr_pending(attr, bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(gs_kernel<G, kCenter, kNT, kPlanes>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    if (e != cudaSuccess) return e;
+    attr.fetch_or(bit);
+  }
+  // a stage holds widths of up to avg_bits + 1 on average; 4 more words where the copy starts early
+  p.cap = GS_K / 32 * std::min(avg_bits + 1, 8) + 4;
+  p.wstride = (p.cap + 7) / 8 * 8 + 4;  // 4 modulo 8: the eight rows of a read meet no bank twice
+  const size_t smem = (size_t)GS_STAGES * (kPlanes * 8 * kNT * GS_XSTRIDE + GS_M * p.wstride * 4);
+  // the depth is split over a cluster until about four CTAs an SM have work
+  const int64_t tiles = slots * p.mtiles, chunks = (p.n + GS_K - 1) / GS_K;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= (int64_t)num_sms * 6 && chunks >= split * 2) split *= 2;
+  p.split = split;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.mtiles * split), (unsigned)slots, 1);
+  cfg.blockDim = dim3(GS_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, gs_kernel<G, kCenter, kNT, kPlanes>, p);
+}
+
+template <int G, bool kCenter>
+static cudaError_t launch_few_of(const GsParams& p, int planes, int64_t slots, int64_t R, int avg_bits, int num_sms,
+                                 cudaStream_t s) {
+  if (planes == 3)
+    return R <= 8 ? launch_few<G, kCenter, 1, 3>(p, slots, avg_bits, num_sms, s)
+                  : launch_few<G, kCenter, 2, 3>(p, slots, avg_bits, num_sms, s);
+  if (R <= 8) return launch_few<G, kCenter, 1, 1>(p, slots, avg_bits, num_sms, s);
+  return R <= 16 ? launch_few<G, kCenter, 2, 1>(p, slots, avg_bits, num_sms, s)
+                 : launch_few<G, kCenter, 4, 1>(p, slots, avg_bits, num_sms, s);
+}
+
 cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const float* scale, const float* zero,
                            int64_t E, int64_t m, int64_t n, int group, int avg_bits, const void* x, int xdtype,
                            int64_t T, const int32_t* row_index, const int32_t* offsets, int64_t R, void* y,
                            int ydtype, uint8_t* ws, int num_sms, cudaStream_t s) {
   const GroupedPlan g = grouped_plan(E, m, n, group, xdtype, row_index != nullptr, R);
-  uint16_t* xs = reinterpret_cast<uint16_t*>(ws);
+  uint16_t* xs = g.slots ? reinterpret_cast<uint16_t*>(ws) : nullptr;
   uint16_t* xg = g.planes ? reinterpret_cast<uint16_t*>(ws + g.off_xg) : nullptr;
   const int k = (int)(n / group);
-  const unsigned blocks = (unsigned)((R + GP_ROWS - 1) / GP_ROWS);
-  const int slots = ydtype == 0 ? 8 : 4;
-  if (slots == 8)
-    gg_prep_kernel<8><<<blocks, GP_ROWS * 32, 0, s>>>(x, xdtype, T, row_index, R, n, group, xg, xs, g.xs_stride);
-  else
-    gg_prep_kernel<4><<<blocks, GP_ROWS * 32, 0, s>>>(x, xdtype, T, row_index, R, n, group, xg, xs, g.xs_stride);
-  count_launches(1);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (xs || xg) {
+    const unsigned blocks = (unsigned)((R + GP_ROWS - 1) / GP_ROWS);
+    if (ydtype == 0)
+      gg_prep_kernel<8><<<blocks, GP_ROWS * 32, 0, s>>>(x, xdtype, T, row_index, R, n, group, xg, xs, g.xs_stride);
+    else
+      gg_prep_kernel<4><<<blocks, GP_ROWS * 32, 0, s>>>(x, xdtype, T, row_index, R, n, group, xg, xs, g.xs_stride);
+    count_launches(1);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t rw = n * avg_bits / 32;
+  // one expert of many rows: the few-rows kernel has nothing to do unless its count is small, which only the
+  // device knows, so both run
+  GsParams f{};
+  f.codes = codes; f.bits = bits; f.scale = scale; f.zero = zero; f.offsets = offsets; f.y = y;
+  f.x = xg ? static_cast<const void*>(xg) : x;
+  f.row_index = xg ? nullptr : row_index;
+  f.T = T; f.plane = R * n;
+  f.m = m; f.n = n; f.R = R; f.rw = rw; f.E = (int)E; f.k = k; f.ydtype = ydtype; f.few_rows = kFewRows;
+  f.mtiles = (int)((m + GS_M - 1) / GS_M);
+  const int planes = xdtype == 0 ? 3 : 1;
+  const int64_t few = std::min<int64_t>(E, R);
+#define SLIM_GS(G)                                                                  \
+  (ydtype == 0 ? launch_few_of<G, true>(f, planes, few, R, avg_bits, num_sms, s)    \
+               : launch_few_of<G, false>(f, planes, few, R, avg_bits, num_sms, s))
+  e = group == 32 ? SLIM_GS(32) : (group == 64 ? SLIM_GS(64) : SLIM_GS(128));
+#undef SLIM_GS
+  if (e != cudaSuccess || g.slots == 0) return e;
   GtParams p{};
   p.codes = codes; p.bits = bits; p.scale = scale; p.zero = zero; p.offsets = offsets; p.y = y;
   p.tiles = ws + g.off_tiles;
-  p.m = m; p.n = n; p.R = R; p.rw = n * avg_bits / 32;
-  p.E = (int)E; p.k = k; p.planes = g.planes ? g.planes : 1; p.few_rows = kFewRows;
+  p.m = m; p.n = n; p.R = R; p.rw = rw;
+  p.E = (int)E; p.k = k; p.planes = planes; p.few_rows = kFewRows;
   p.max_slots = (int)g.slots;
+  const int slots = ydtype == 0 ? 8 : 4;
   GtMaps tm;
   const void* xb = xg ? static_cast<const void*>(xg) : x;
   const uint64_t rows = xg ? (uint64_t)g.planes * R : (uint64_t)T;
