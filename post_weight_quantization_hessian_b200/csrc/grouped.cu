@@ -187,10 +187,10 @@ constexpr int GD_THREADS = 256, GD_BOXES = 16;
 
 template <int B, bool kCenter>
 __device__ __forceinline__ uint4 decode8(uint32_t lo, uint32_t hi) {
-  uint32_t w[B], o[16];
-#pragma unroll
-  for (int q = 0; q < B; ++q) w[q] = q == 0 ? lo : (q == 1 ? hi : 0u);
-  decode32<B, kCenter>(w, o);  // (only the first 8 codes are kept: the rest is dropped at compile time)
+  uint32_t w[(B * 8 + 31) / 32], o[4];
+  w[0] = lo;
+  if constexpr (B > 4) w[1] = hi;
+  decode_codes<B, 8, kCenter>(w, o);
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -716,13 +716,14 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
 // chunks; the CTAs of a cluster share the outputs and split the depth, and add
 // their sums through distributed shared memory in a fixed order. Codes and x
 // arrive by asynchronous copies, two chunks ahead; scales and zeros go through
-// registers one chunk ahead. In a 32-column unit thread (g, t) of a warp takes
-// the 8 codes 8 t .. 8 t + 7 of rows g, g + 8, g + 16, g + 24: as k-steps may
-// take the columns in any order that x follows, those are its four pairs of two
-// k-steps, and x's are 16 consecutive bytes. The group sums of x are the product
-// with a row of ones.
-constexpr int GS_THREADS = 128, GS_M = 128, GS_K = 256, GS_STAGES = 3;
-constexpr int GS_XSTRIDE = GS_K * 2 + 64;  // bytes of a row of x: eight rows' 16-byte reads meet no bank twice
+// registers one chunk ahead. Of 64 columns (32 in groups of 32) thread (g, t) of a
+// warp takes the 16 (8) codes from 16 t (8 t) on of rows g, g + 8, g + 16, g + 24:
+// as k-steps may take the columns in any order that x follows, those are its
+// pairs of four (two) k-steps, and x's are consecutive bytes. The group sums of
+// x are the product with a row of ones.
+constexpr int GS_THREADS = 128, GS_M = 128, GS_K = 256, GS_STAGES = 2;
+// Bytes of a row of x: the 16-byte reads of two rows and four threads meet no bank twice.
+__host__ __device__ constexpr int gs_xstride(int group) { return GS_K * 2 + (group == 32 ? 64 : 16); }
 
 struct GsParams {
   const uint32_t* codes;
@@ -758,10 +759,13 @@ __device__ __forceinline__ void gs_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
 template <int G, bool kCenter, int kNT, int kPlanes>
 __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
   constexpr int kUnits = G / 32, kGroups = GS_K / G, kRows = 8 * kNT;
+  constexpr int kSub = G == 32 ? 32 : 64, kCodes = kSub / 4;  // columns decoded at a time, and a thread's of a row
+  constexpr int GS_XSTRIDE = gs_xstride(G);
   extern __shared__ __align__(16) uint8_t gs_smem[];
   __shared__ int s_expert, s_found;
   __shared__ uint32_t s_width[1024];               // first word << 4 | width of each group
   __shared__ float2 s_coef[2][kGroups][GS_M];      // coef_d, coef_x
+  __shared__ int s_row[kRows];                     // row of x, -1: zeros
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int rank = blockIdx.x % p.split, mt = blockIdx.x / p.split;
   // the expert of this slot among those with 1 .. few_rows rows
@@ -831,35 +835,56 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
       for (int b = 0; b < kNT; ++b)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[a][b][c] = 0.f;
+    if (tid < kRows) {
+      int src = q0 + tid;
+      if (tid < rows && p.row_index) src = p.row_index[src];
+      s_row[tid] = tid < rows && src >= 0 && src < p.T ? src : -1;
+    }
+    __syncthreads();
+    const uint32_t* codes0 = p.codes + (base + m0 + (tid >> 3)) * p.rw;
     auto copy_chunk = [&](int ch, int slot) {
       if (ch < ch1) {
         const uint32_t sx = sbase + slot * stage, sw = sx + xbytes;
         const int cols = (int)min((int64_t)GS_K, p.n - (int64_t)ch * GS_K);
-        for (int v = tid; v < kPlanes * nt * 8 * 32; v += GS_THREADS) {
-          const int c = v & 31, r = v >> 5, pl = kPlanes > 1 ? r / (nt * 8) : 0, rr = kPlanes > 1 ? r - pl * (nt * 8) : r;
-          int64_t src = q0 + rr;
-          bool have = rr < rows && c * 8 < cols;
-          if (have && p.row_index) {
-            src = p.row_index[src];
-            have = src >= 0 && src < p.T;
+        const int c = tid & 31;
+        const bool col_ok = c * 8 < cols;
+#pragma unroll
+        for (int pl = 0; pl < kPlanes; ++pl)
+#pragma unroll 2
+          for (int r = tid >> 5; r < nt * 8; r += GS_THREADS / 32) {
+            const int src = s_row[r];
+            const bool have = src >= 0 && col_ok;
+            gs_cp16(sx + (pl * kRows + r) * GS_XSTRIDE + c * 16,
+                    static_cast<const uint16_t*>(p.x) + pl * p.plane + (have ? src * p.n + ch * GS_K + c * 8 : 0),
+                    have ? 16u : 0u);  // 0: zeros
           }
-          if (!have) src = 0;
-          gs_cp16(sx + (pl * kRows + rr) * GS_XSTRIDE + c * 16,
-                  static_cast<const uint16_t*>(p.x) + pl * p.plane + src * p.n + (have ? ch * GS_K + c * 8 : 0),
-                  have ? 16u : 0u);  // 0: zeros
-        }
         int first, end;
         chunk_words(ch, first, end);
         end = min(end, first + p.cap);
-        const uint32_t* src = p.codes + (base + m0) * p.rw;
+        const int row = tid >> 3;  // and every 16th from it
+        const uint32_t rstep = 16 * p.wstride * 4;
         if (wide) {
-          for (int r = tid >> 3; r < mrows; r += GS_THREADS / 8)
-            for (int w = first + (tid & 7) * 4; w < end; w += 32)
-              gs_cp16(sw + (r * p.wstride + w - first) * 4, src + (int64_t)r * p.rw + w, 16u);
+          for (int w = (tid & 7) * 4; w < end - first; w += 32) {
+            const uint32_t* src = codes0 + first + w;
+            uint32_t dst = sw + (row * p.wstride + w) * 4;
+#pragma unroll
+            for (int i = 0; i < GS_M / 16; ++i) {
+              if (row + 16 * i < mrows) gs_cp16(dst, src, 16u);
+              src += 16 * p.rw;
+              dst += rstep;
+            }
+          }
         } else {
-          for (int r = tid >> 3; r < mrows; r += GS_THREADS / 8)
-            for (int w = first + (tid & 7); w < end; w += 8)
-              gs_cp4(sw + (r * p.wstride + w - first) * 4, src + (int64_t)r * p.rw + w);
+          for (int w = tid & 7; w < end - first; w += 8) {
+            const uint32_t* src = codes0 + first + w;
+            uint32_t dst = sw + (row * p.wstride + w) * 4;
+#pragma unroll
+            for (int i = 0; i < GS_M / 16; ++i) {
+              if (row + 16 * i < mrows) gs_cp4(dst, src);
+              src += 16 * p.rw;
+              dst += rstep;
+            }
+          }
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -873,8 +898,8 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
         zreg[c] = __ldg(p.zero + srow + at);
       }
     };
-    copy_chunk(ch0, 0);
-    copy_chunk(ch0 + 1, 1);
+#pragma unroll
+    for (int c = 0; c < GS_STAGES - 1; ++c) copy_chunk(ch0 + c, c);
     if (ch0 < ch1) load_scales(ch0);
     int slot = 0;
     for (int ch = ch0; ch < ch1; ++ch) {
@@ -886,12 +911,12 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
                                    : make_float2(0.f, 0.f);
       }
       if (ch + 1 < ch1) load_scales(ch + 1);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(GS_STAGES - 2) : "memory");
       __syncthreads();  // this chunk has arrived for all; the slot of the last one is free
-      copy_chunk(ch + 2, slot == 0 ? 2 : slot - 1);
+      copy_chunk(ch + GS_STAGES - 1, slot == 0 ? GS_STAGES - 1 : slot - 1);
       int first, end;
       chunk_words(ch, first, end);
-      const uint32_t sx = sbase + slot * stage + g * GS_XSTRIDE + t4 * 16;
+      const uint32_t sx = sbase + slot * stage + g * GS_XSTRIDE + t4 * kCodes * 2;
       const uint32_t sw = sbase + slot * stage + xbytes + (warp * 32 + g) * p.wstride * 4;
       const bool fits = end - first <= p.cap;
 #pragma unroll 1
@@ -904,62 +929,64 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
         for (int q = 0; q < kNT; ++q)
 #pragma unroll
           for (int v = 0; v < 4; ++v) d[0][q][v] = d[1][q][v] = xs[q][v] = 0.f;
-        const int wrel = (int)(en >> 4) - first;
+        const uint32_t wrel = (en >> 4) - first;
 #pragma unroll 1
-        for (int u = 0; u < kUnits; ++u) {
-          // 8 codes (b bytes) of four rows
-          const uint32_t bit = (uint32_t)(wrel + u * b) * 32 + t4 * 8 * b, sh = bit & 31;
-          uint32_t lo[4], hi[4], A[4][4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            uint32_t w0, w1 = 0, w2 = 0;
-            if (fits) {
-              const uint32_t at = sw + r * 8 * p.wstride * 4 + (bit >> 5) * 4;
-              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(at));
-              if (b == 3 || b > 4) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w1) : "r"(at + 4));
-              if (b > 4) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w2) : "r"(at + 8));
-            } else {  // wider than the stage was made for: straight from global memory
-              const int row = min(warp * 32 + g + 8 * r, mrows - 1);
-              const uint32_t* src = p.codes + (base + m0 + row) * p.rw;
-              const int64_t w = first + (bit >> 5);
-              w0 = w < p.rw ? __ldg(src + w) : 0u;
-              w1 = w + 1 < p.rw ? __ldg(src + w + 1) : 0u;
-              w2 = w + 2 < p.rw ? __ldg(src + w + 2) : 0u;
-            }
-            lo[r] = __funnelshift_r(w0, w1, sh);
-            hi[r] = __funnelshift_r(w1, w2, sh);
-          }
+        for (int u = 0; u < G / kSub; ++u) {
+          // the thread's kCodes codes of four rows: kCodes b bits from bit `bit` of the staged row on
+          const uint32_t bit = (wrel + u * (kSub / 32) * b) * 32 + t4 * kCodes * b;
+          uint32_t A[4][kCodes / 2];
           switch (b) {
-#define GS_CASE(B)                                                      \
-  case B:                                                               \
-    _Pragma("unroll") for (int r = 0; r < 4; ++r) {                     \
-      const uint4 v = decode8<B, kCenter>(lo[r], hi[r]);                \
-      A[r][0] = v.x; A[r][1] = v.y; A[r][2] = v.z; A[r][3] = v.w;       \
-    }                                                                   \
-    break;
+#define GS_CASE(B)                                                                                            \
+  case B: {                                                                                                   \
+    constexpr int kBits = B * kCodes, kWords = (kBits + 31) / 32;                                             \
+    /* the bits start where a multiple of kBits and of 8 can start in a word */                               \
+    constexpr bool kShift = kBits % 32 != 0, kMore = kShift && (kBits % 32) + (kBits % 16 ? 24 : 16) > 32;    \
+    const uint32_t sh = bit & 31;                                                                             \
+    _Pragma("unroll") for (int r = 0; r < 4; ++r) {                                                           \
+      uint32_t w[kWords + 1], v[kWords];                                                                      \
+      w[kWords] = 0;                                                                                          \
+      if (fits) {                                                                                             \
+        const uint32_t at = sw + (r * 8 * p.wstride + (bit >> 5)) * 4;                                        \
+        _Pragma("unroll") for (int q = 0; q < kWords + (kMore ? 1 : 0); ++q)                                  \
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[q]) : "r"(at + 4 * q));                           \
+      } else { /* wider than the stage was made for: straight from global memory */                           \
+        const int row = min(warp * 32 + g + 8 * r, mrows - 1);                                                \
+        const uint32_t* src = p.codes + (base + m0 + row) * p.rw;                                             \
+        _Pragma("unroll") for (int q = 0; q < kWords + (kMore ? 1 : 0); ++q) {                                \
+          const int64_t at = first + (bit >> 5) + q;                                                          \
+          w[q] = at < p.rw ? __ldg(src + at) : 0u;                                                            \
+        }                                                                                                     \
+      }                                                                                                       \
+      _Pragma("unroll") for (int q = 0; q < kWords; ++q) v[q] = kShift ? __funnelshift_r(w[q], w[q + 1], sh) : w[q]; \
+      decode_codes<B, kCodes, kCenter>(v, A[r]);                                                              \
+    }                                                                                                         \
+  } break;
             GS_CASE(1) GS_CASE(2) GS_CASE(3) GS_CASE(4) GS_CASE(5) GS_CASE(6) GS_CASE(7) GS_CASE(8)
 #undef GS_CASE
-            default:
-#pragma unroll
-              for (int r = 0; r < 4; ++r) A[r][0] = A[r][1] = A[r][2] = A[r][3] = 0u;
+            default: break;
           }
-          const uint32_t xu = sx + (c * kUnits + u) * 64;
+          const uint32_t xu = sx + (c * G + u * kSub) * 2;
 #pragma unroll
           for (int pl = kPlanes - 1; pl >= 0; --pl)
 #pragma unroll
             for (int q = 0; q < kNT; ++q)
               if (q < nt) {
-                uint32_t b0, b1, b2, b3;
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
-                             : "r"(xu + (pl * kRows + q * 8) * GS_XSTRIDE));
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {
-                  gs_mma(d[a][q], A[2 * a][0], A[2 * a + 1][0], A[2 * a][1], A[2 * a + 1][1], b0, b1);
-                  gs_mma(d[a][q], A[2 * a][2], A[2 * a + 1][2], A[2 * a][3], A[2 * a + 1][3], b2, b3);
+                for (int h = 0; h < kCodes / 8; ++h) {
+                  uint32_t b0, b1, b2, b3;
+                  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                               : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
+                               : "r"(xu + (pl * kRows + q * 8) * GS_XSTRIDE + h * 16));
+#pragma unroll
+                  for (int a = 0; a < 2; ++a) {
+                    gs_mma(d[a][q], A[2 * a][4 * h], A[2 * a + 1][4 * h], A[2 * a][4 * h + 1], A[2 * a + 1][4 * h + 1],
+                           b0, b1);
+                    gs_mma(d[a][q], A[2 * a][4 * h + 2], A[2 * a + 1][4 * h + 2], A[2 * a][4 * h + 3],
+                           A[2 * a + 1][4 * h + 3], b2, b3);
+                  }
+                  gs_mma(xs[q], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, b0, b1);
+                  gs_mma(xs[q], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, b2, b3);
                 }
-                gs_mma(xs[q], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, b0, b1);
-                gs_mma(xs[q], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, b2, b3);
               }
         }
 #pragma unroll
@@ -974,7 +1001,7 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
             }
         }
       }
-      slot = slot == 2 ? 0 : slot + 1;
+      slot = slot == GS_STAGES - 1 ? 0 : slot + 1;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
@@ -1024,7 +1051,7 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
 }
 
 // ---------------------------------------------------------------- host side
-constexpr int kFewRows = 32;  // experts with at most this many rows: the few-rows kernel
+constexpr int kFewRows = 64;  // experts with at most this many rows: the few-rows kernel
 constexpr size_t kTileBytes = size_t(64) << 20;  // decoded tiles of a pass: they stay in L2 (126 MB)
 
 struct GroupedPlan {
@@ -1093,7 +1120,7 @@ static cudaError_t launch_few(GsParams p, int64_t slots, int avg_bits, int num_s
   // a stage holds widths of up to avg_bits + 1 on average; 4 more words where the copy starts early
   p.cap = GS_K / 32 * std::min(avg_bits + 1, 8) + 4;
   p.wstride = (p.cap + 7) / 8 * 8 + 4;  // 4 modulo 8: the eight rows of a read meet no bank twice
-  const size_t smem = (size_t)GS_STAGES * (kPlanes * 8 * kNT * GS_XSTRIDE + GS_M * p.wstride * 4);
+  const size_t smem = (size_t)GS_STAGES * (kPlanes * 8 * kNT * gs_xstride(G) + GS_M * p.wstride * 4);
   // the depth is split over a cluster until about four CTAs an SM have work
   const int64_t tiles = slots * p.mtiles, chunks = (p.n + GS_K - 1) / GS_K;
   int split = 1;
@@ -1152,7 +1179,7 @@ cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const flo
   f.codes = codes; f.bits = bits; f.scale = scale; f.zero = zero; f.offsets = offsets; f.y = y;
   f.x = xg ? static_cast<const void*>(xg) : x;
   f.row_index = xg ? nullptr : row_index;
-  f.T = T; f.plane = R * n;
+  f.T = xg ? R : T; f.plane = R * n;
   f.m = m; f.n = n; f.R = R; f.rw = rw; f.E = (int)E; f.k = k; f.ydtype = ydtype; f.few_rows = kFewRows;
   f.mtiles = (int)((m + GS_M - 1) / GS_M);
   const int planes = xdtype == 0 ? 3 : 1;
