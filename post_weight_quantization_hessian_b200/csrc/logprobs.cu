@@ -4,25 +4,36 @@
 //   top     = the top_k largest logits (equal values: the lower index first),
 //             as l - lse and their indices.
 //
-// This kernel is the plain one: a block per row, a pass for the maximum, one
-// for the sums and one more for each alternative.
+// One pass over the row. A thread keeps the maximum m of its elements and, relative
+// to it, S = sum e^(l - m) and T = sum (l - m) e^(l - m); a larger maximum m'
+// rescales both, T' = (T + (m - m') S) e^(m - m'). Partial results join the same
+// way, and logp = l - m - log S, entropy = log S - T / S.
+//
+// The alternatives come from the same pass. With at least 32 groups of elements
+// (the lanes of all warps), the top_k-th largest of the groups' maxima is a bound
+// that at least top_k elements reach and that few others do (about 30 in all for
+// 20 of 32 groups in random order). Only threads whose own maximum reaches it look
+// at their elements again; what they collect is ranked by counting. Values are
+// compared with their index as one 64-bit key, so ties are decided and equal rows
+// collect no more than others. Rows that put too many large elements into few
+// groups, and rows with a NaN, take one scan for each alternative instead.
+//
+// Bound by the bytes of the logits for many rows (about 5.5 issued operations an
+// element in packed pairs); for few rows a cluster of up to 8 CTAs shares a row, as one CTA
+// cannot ask for the bytes fast enough, and joins through distributed shared memory.
 #include <cstdint>
 #include "common.cuh"
 
 namespace slim {
 
-constexpr int LP_THREADS = 256;
-
-__device__ __forceinline__ float lp_ld(const void* p, int64_t i, int dtype) {
-  if (dtype == 0) return static_cast<const float*>(p)[i];
-  return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-}
+constexpr int LP_MAX_K = 32;
+constexpr int LP_CAND = 1024;  // collected elements; more take the scans
 
 // A 64-bit key that orders (value, index): larger value first, then the lower
-// index; NaN above everything, -0 equal to +0.
+// index; NaN above everything, -0 equal to +0. No key is 0 or all ones.
 __device__ __forceinline__ uint64_t lp_key(float v, uint32_t idx) {
   v = v + 0.f;
-  uint32_t u = v != v ? 0x7FFFFFFFu : __float_as_uint(v);
+  uint32_t u = v != v ? 0x7FC00000u : __float_as_uint(v);
   u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
   return ((uint64_t)u << 32) | (uint32_t)~idx;
 }
@@ -30,68 +41,382 @@ __device__ __forceinline__ float lp_key_value(uint64_t key) {
   const uint32_t u = (uint32_t)(key >> 32);
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
 }
-
-template <typename T, typename Op>
-__device__ T lp_block(T v, T* red, Op op) {
-  __syncthreads();
-  red[threadIdx.x] = v;
-  __syncthreads();
-  for (int o = LP_THREADS / 2; o > 0; o >>= 1) {
-    if (threadIdx.x < o) red[threadIdx.x] = op(red[threadIdx.x], red[threadIdx.x + o]);
-    __syncthreads();
-  }
-  return red[0];
+__device__ __forceinline__ uint64_t lp_max(uint64_t a, uint64_t b) { return a > b ? a : b; }
+__device__ __forceinline__ float lp_max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float lp_ex2(float a) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint64_t lp_pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void lp_unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t lp_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t lp_mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t lp_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
 }
 
-__global__ void __launch_bounds__(LP_THREADS)
-lp_plain_kernel(const void* __restrict__ logits, int dtype, int64_t V, int64_t ld, const int64_t* __restrict__ tokens,
-                int top_k, float* __restrict__ logp, float* __restrict__ entropy, float* __restrict__ top_logp,
-                int32_t* __restrict__ top_id) {
-  __shared__ uint64_t red[LP_THREADS];
-  const int64_t row = blockIdx.x, at = row * ld;
-  auto max64 = [](uint64_t a, uint64_t b) { return a > b ? a : b; };
-  auto add = [](float a, float b) { return a + b; };
-  uint64_t best = 0;
-  for (int64_t v = threadIdx.x; v < V; v += LP_THREADS) best = max64(best, lp_key(lp_ld(logits, at + v, dtype), (uint32_t)v));
-  best = lp_block(best, red, max64);
-  const float top = lp_key_value(best);
-  const float base = top == -INFINITY ? 0.f : top;
-  float S = 0.f, Tsum = 0.f;
-  for (int64_t v = threadIdx.x; v < V; v += LP_THREADS) {
-    const float d = lp_ld(logits, at + v, dtype) - base, e = expf(d);
-    S += e;
-    if (e != 0.f) Tsum += e * d;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFar = -150.f;  // e^-150 is 0 in fp32; keeps 0 * -inf out of T
+
+struct LpStat {
+  float m, S, T;
+  // Relative to a larger maximum. (An m of -inf goes with S = T = 0.)
+  __device__ __forceinline__ void rise(float to) {
+    const float dm = fmaxf(m - to, -1e4f), f = lp_ex2(dm * kLog2e);
+    T = (T + S * dm) * f;
+    S *= f;
+    m = to;
   }
-  S = lp_block(S, reinterpret_cast<float*>(red), add);
-  Tsum = lp_block(Tsum, reinterpret_cast<float*>(red), add);
-  const float ls = S == 0.f ? 0.f : logf(S);
-  if (threadIdx.x == 0) {
-    const int64_t t = tokens ? tokens[row] : -1;
-    if (logp) logp[row] = t >= 0 && t < V ? lp_ld(logits, at + t, dtype) - base - ls : 0.f;
-    if (entropy) entropy[row] = S == 0.f ? 0.f : ls - Tsum / S;
+  __device__ __forceinline__ void join(LpStat o) {
+    if (o.m > m) rise(o.m);
+    else if (m > o.m) o.rise(m);
+    S += o.S;
+    T += o.T;
   }
-  for (int q = 0; q < top_k; ++q) {
-    if (threadIdx.x == 0) {
-      top_logp[row * top_k + q] = lp_key_value(best) - base - ls;
-      top_id[row * top_k + q] = (int32_t)~(uint32_t)best;
+};
+
+template <typename E>
+__device__ __forceinline__ float lp_load(const E* p) {
+  if constexpr (sizeof(E) == 4)
+    return __ldg(reinterpret_cast<const float*>(p));
+  else
+    return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p)) << 16);
+}
+// The kVec elements of a 16-byte vector.
+template <typename E, int kVec>
+__device__ __forceinline__ void lp_unpack(const uint4& q, float (&v)[kVec]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(E) == 4) {
+      v[i] = __uint_as_float(w[i]);
+    } else {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
-    const uint64_t last = best;
-    best = 0;
-    for (int64_t v = threadIdx.x; v < V; v += LP_THREADS) {
-      const uint64_t key = lp_key(lp_ld(logits, at + v, dtype), (uint32_t)v);
-      if (key < last && key > best) best = key;
-    }
-    best = lp_block(best, red, max64);
   }
+}
+
+template <typename E, int kThreads>
+__global__ void __launch_bounds__(kThreads)
+lp_kernel(const E* __restrict__ logits, int64_t V, int64_t ld, const int64_t* __restrict__ tokens, int top_k,
+          int split, float* __restrict__ logp, float* __restrict__ entropy, float* __restrict__ top_logp,
+          int32_t* __restrict__ top_id) {
+  constexpr int kVec = 16 / sizeof(E), kWarps = kThreads / 32, kBatch = 4;
+  __shared__ LpStat s_stat[kWarps];
+  __shared__ LpStat s_cta;
+  __shared__ uint64_t s_best[kWarps][32];
+  __shared__ uint64_t s_cand[LP_CAND];
+  __shared__ uint64_t s_out[LP_MAX_K];
+  __shared__ uint64_t s_bound;
+  __shared__ int s_count;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = blockIdx.x / split;
+  const int rank = (int)(blockIdx.x - row * split);
+  const E* x = logits + row * ld;
+  // this CTA's part: whole 16-byte vectors, the first CTA also what lies before the
+  // first of them, the last one what lies behind the last
+  const uint32_t mis = (uint32_t)(reinterpret_cast<uintptr_t>(x) & 15) / sizeof(E);
+  const uint32_t head = (uint32_t)min((int64_t)(mis ? kVec - mis : 0), V);
+  const uint32_t nvec = (uint32_t)((V - head) / kVec), tail = head + nvec * kVec;
+  const uint32_t v0 = (uint32_t)((uint64_t)nvec * rank / split), v1 = (uint32_t)((uint64_t)nvec * (rank + 1) / split);
+  const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+  int64_t token = -1;
+  float given = 0.f;
+  if (tid == 0 && rank == 0 && tokens) {
+    token = tokens[row];
+    if (token >= 0 && token < V) given = lp_load(x + token);
+  }
+  // a scalar element of this thread: one of the head, before its vectors, or one of the tail, behind them
+  const bool in_head = rank == 0 && tid < head;
+  const bool in_tail = rank == split - 1 && tid >= 32 && tail + (tid - 32) < V;  // (kVec < 32 of them)
+  const int64_t odd = in_head ? tid : (in_tail ? (int64_t)tail + (tid - 32) : -1);
+  const float odd_value = odd >= 0 ? lp_load(x + odd) : 0.f;
+  auto single = [](float v) {
+    return LpStat{v == v ? v : -INFINITY, v == INFINITY || v != v ? NAN : (v == -INFINITY ? 0.f : 1.f), 0.f};
+  };
+  LpStat st = {-INFINITY, 0.f, 0.f};
+  uint32_t first_max = 0;  // the index of the thread's maximum, its first
+  bool any = in_head;
+  if (in_head) {
+    st = single(odd_value);
+    first_max = (uint32_t)odd;
+  }
+  for (uint32_t i = v0 + tid; i < v1; i += kThreads * kBatch) {
+    uint4 q[kBatch];
+    float v[kVec];
+    const uint32_t left = (v1 - i + kThreads - 1) / kThreads;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (b < left) q[b] = __ldg(xv + i + b * kThreads);
+    float top = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (b < left) {
+        lp_unpack<E, kVec>(q[b], v);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) top = fmaxf(top, v[j]);
+      }
+    if (top > st.m) {
+      if (st.m == -INFINITY) st.m = top; else st.rise(top);
+      bool found = false;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (b < left) {
+          lp_unpack<E, kVec>(q[b], v);
+#pragma unroll
+          for (int j = 0; j < kVec; ++j)
+            if (!found && v[j] == top) {
+              found = true;
+              first_max = head + (i + b * kThreads) * kVec + j;
+            }
+        }
+    } else if (!any) {
+      first_max = head + i * kVec;  // nothing above -inf: the first element stands for the thread
+    }
+    any = true;
+    const float base = st.m == -INFINITY ? 0.f : -st.m;
+    const uint64_t base2 = lp_pair(base, base), l2 = lp_pair(kLog2e, kLog2e);
+    uint64_t S2 = 0ull, T2 = 0ull;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (b < left) {
+        lp_unpack<E, kVec>(q[b], v);
+#pragma unroll
+        for (int j = 0; j < kVec; j += 2) {
+          float d0, d1, e0, e1;
+          lp_unpair(lp_add2(lp_pair(v[j], v[j + 1]), base2), d0, d1);
+          const uint64_t d = lp_pair(lp_max_nan(d0, kFar), lp_max_nan(d1, kFar));
+          lp_unpair(lp_mul2(d, l2), e0, e1);
+          const uint64_t e = lp_pair(lp_ex2(e0), lp_ex2(e1));
+          S2 = lp_add2(S2, e);
+          T2 = lp_fma2(e, d, T2);
+        }
+      }
+    float a, b;
+    lp_unpair(S2, a, b);
+    st.S += a + b;
+    lp_unpair(T2, a, b);
+    st.T += a + b;
+  }
+  if (in_tail) {
+    if (!any || odd_value > st.m) first_max = (uint32_t)odd;
+    st.join(single(odd_value));
+    any = true;
+  }
+  const uint64_t mine = any ? lp_key(st.m, first_max) : 0ull;
+
+  // the CTA's statistics, in a fixed order
+  LpStat w = st;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    LpStat other = {__shfl_xor_sync(0xffffffffu, w.m, o), __shfl_xor_sync(0xffffffffu, w.S, o),
+                    __shfl_xor_sync(0xffffffffu, w.T, o)};
+    w.join(other);
+  }
+  if (lane == 0) s_stat[warp] = w;
+  if (top_k) s_best[warp][lane] = mine;
+  if (tid == 0) s_count = 0;
+  __syncthreads();
+  if (warp == 0) {
+    LpStat c = lane < kWarps ? s_stat[lane] : LpStat{-INFINITY, 0.f, 0.f};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      LpStat other = {__shfl_xor_sync(0xffffffffu, c.m, o), __shfl_xor_sync(0xffffffffu, c.S, o),
+                      __shfl_xor_sync(0xffffffffu, c.T, o)};
+      c.join(other);
+    }
+    if (lane == 0) s_cta = c;
+    if (top_k) {
+      uint64_t g = 0;
+#pragma unroll
+      for (int u = 0; u < kWarps; ++u) g = lp_max(g, s_best[u][lane]);
+      int above = 0;
+#pragma unroll
+      for (int u = 0; u < 32; ++u) {
+        const uint64_t o = __shfl_sync(0xffffffffu, g, u);
+        above += o > g || (o == g && u < lane) ? 1 : 0;
+      }
+      if (above == top_k - 1) s_bound = g;
+    }
+  }
+  __syncthreads();
+  if (top_k) {
+    const uint64_t bound = s_bound;
+    bool scan = s_cta.S != s_cta.S;  // a NaN or +inf
+    if (!scan) {
+      if (any && mine >= bound) {
+        auto offer = [&](float v, uint32_t idx) {
+          const uint64_t key = lp_key(v, idx);
+          if (key >= bound) {
+            const int at = atomicAdd(&s_count, 1);  // (the order does not matter: keys are ranked)
+            if (at < LP_CAND) s_cand[at] = key;
+          }
+        };
+        if (odd >= 0) offer(odd_value, (uint32_t)odd);
+        for (uint32_t i = v0 + tid; i < v1; i += kThreads) {
+          float v[kVec];
+          lp_unpack<E, kVec>(__ldg(xv + i), v);
+          float top = v[0];
+#pragma unroll
+          for (int j = 1; j < kVec; ++j) top = fmaxf(top, v[j]);
+          if (lp_key(top, 0u) >= bound) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) offer(v[j], head + i * kVec + j);
+          }
+        }
+      }
+      __syncthreads();
+      const int count = s_count;
+      scan = count > LP_CAND;
+      if (!scan) {
+        if (tid < LP_MAX_K) s_out[tid] = 0ull;
+        __syncthreads();
+        for (int c = tid; c < count; c += kThreads) {
+          const uint64_t key = s_cand[c];
+          int above = 0;
+          for (int u = 0; u < count; ++u) above += s_cand[u] > key ? 1 : 0;
+          if (above < top_k) s_out[above] = key;
+        }
+      }
+    }
+    if (scan) {  // (uniform) one scan for each alternative
+      uint64_t last = ~0ull;
+      for (int r = 0; r < top_k; ++r) {
+        uint64_t best = 0;
+        auto offer = [&](float v, uint32_t idx) {
+          const uint64_t key = lp_key(v, idx);
+          if (key < last && key > best) best = key;
+        };
+        if (odd >= 0) offer(odd_value, (uint32_t)odd);
+        for (uint32_t i = v0 + tid; i < v1; i += kThreads) {
+          float v[kVec];
+          lp_unpack<E, kVec>(__ldg(xv + i), v);
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) offer(v[j], head + i * kVec + j);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) best = lp_max(best, __shfl_xor_sync(0xffffffffu, best, o));
+        __syncthreads();
+        if (lane == 0) s_best[0][warp] = best;
+        __syncthreads();
+        best = 0;
+        for (int u = 0; u < kWarps; ++u) best = lp_max(best, s_best[0][u]);
+        if (tid == 0) s_out[r] = best;
+        last = best;
+      }
+    }
+    __syncthreads();
+  }
+  // the row's statistics and alternatives, by the first CTA of a cluster
+  if (split > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  if (rank == 0) {
+    LpStat c = s_cta;
+    if (split > 1) {
+      const uint32_t at = smem_u32(&s_cta), out = smem_u32(s_out);
+      for (int z = 1; z < split; ++z) {
+        uint32_t r;
+        LpStat o;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(z));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.m) : "r"(r) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.S) : "r"(r + 4) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o.T) : "r"(r + 8) : "memory");
+        c.join(o);
+      }
+      if (top_k) {
+        for (int v = tid; v < split * top_k; v += kThreads) {
+          const int z = v / top_k;
+          uint32_t r;
+          uint64_t key;
+          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(out + (v - z * top_k) * 8), "r"(z));
+          asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(key) : "r"(r) : "memory");
+          s_cand[v] = key;
+        }
+        __syncthreads();
+        for (int v = tid; v < split * top_k; v += kThreads) {
+          const uint64_t key = s_cand[v];
+          int above = 0;
+          for (int u = 0; u < split * top_k; ++u) above += s_cand[u] > key ? 1 : 0;
+          if (key && above < top_k) s_out[above] = key;
+        }
+        __syncthreads();
+      }
+    }
+    const float base = c.m == -INFINITY ? 0.f : c.m;
+    const float log_sum = c.S == 0.f ? 0.f : logf(c.S);  // (NaN stays NaN)
+    if (tid == 0) {
+      if (logp) logp[row] = token >= 0 && token < V ? given - base - log_sum : 0.f;
+      if (entropy) entropy[row] = c.S == 0.f ? 0.f : log_sum - c.T / c.S;
+    }
+    if (tid < top_k) {
+      const uint64_t key = s_out[tid];
+      top_logp[row * top_k + tid] = lp_key_value(key) - base - log_sum;
+      top_id[row * top_k + tid] = (int32_t)~(uint32_t)key;
+    }
+  }
+  if (split > 1) {  // no CTA leaves while the first may still read its results
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+
+template <typename E, int kThreads>
+static cudaError_t launch_lp(const void* logits, int64_t N, int64_t V, int64_t ld, const int64_t* tokens, int top_k,
+                             int split, float* logp, float* entropy, float* top_logp, int32_t* top_id,
+                             cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(N * split), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, lp_kernel<E, kThreads>, static_cast<const E*>(logits), V, ld, tokens, top_k, split,
+                            logp, entropy, top_logp, top_id);
 }
 
 cudaError_t launch_logprobs(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const int64_t* tokens,
                             int top_k, float* logp, float* entropy, float* top_logp, int32_t* top_id, int num_sms,
                             cudaStream_t s) {
-  lp_plain_kernel<<<(unsigned)N, LP_THREADS, 0, s>>>(logits, dtype, V, ld, tokens, top_k, logp, entropy, top_logp,
-                                                     top_id);
-  count_launches(1);
-  return cudaGetLastError();
+  const int64_t bytes = V * (dtype == 0 ? 4 : 2);
+  // a row is split until there are two CTAs an SM, while each part is worth a CTA
+  int split = 1;
+  while (split < 8 && N * split < 2 * num_sms && bytes / (2 * split) >= 8192) split *= 2;
+  const bool small = bytes / split <= 16384;
+#define SLIM_LP(E)                                                                                                    \
+  (small ? launch_lp<E, 128>(logits, N, V, ld, tokens, top_k, split, logp, entropy, top_logp, top_id, s)             \
+         : launch_lp<E, 512>(logits, N, V, ld, tokens, top_k, split, logp, entropy, top_logp, top_id, s))
+  return dtype == 0 ? SLIM_LP(float) : SLIM_LP(uint16_t);
+#undef SLIM_LP
 }
 
 }  // namespace slim
