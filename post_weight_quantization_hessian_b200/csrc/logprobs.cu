@@ -9,19 +9,21 @@
 // rescales both, T' = (T + (m - m') S) e^(m - m'). Partial results join the same
 // way, and logp = l - m - log S, entropy = log S - T / S.
 //
-// The alternatives come from the same pass. With at least 32 groups of elements
-// (the lanes of all warps), the top_k-th largest of the groups' maxima is a bound
-// that at least top_k elements reach and that few others do (about 30 in all for
-// 20 of 32 groups in random order). Only threads whose own maximum reaches it look
-// at their elements again; what they collect is ranked by counting. Values are
-// compared with their index as one 64-bit key, so ties are decided and equal rows
-// collect no more than others. Rows that put too many large elements into few
-// groups, and rows with a NaN, take one scan for each alternative instead.
+// The alternatives come from the same pass. Of 32 groups of elements (the lanes of
+// all warps) the top_k-th largest maximum is a bound that at least top_k elements
+// reach and that few others do (about 30 in all for 20 of 32 groups in random
+// order). Only threads whose own maximum reaches it look at their elements again;
+// what they collect is ranked by counting, as 64-bit keys of value and index.
+// Where the bound is -inf (fewer unmasked elements than that), only the others are
+// collected and the lowest masked indices follow them. Rows that put too many
+// elements at or above the bound (long ties, all large ones in few groups) and
+// rows with a NaN take one scan for each alternative instead.
 //
 // Bound by the bytes of the logits for many rows (about 5.5 issued operations an
 // element in packed pairs); for few rows a cluster of up to 8 CTAs shares a row, as one CTA
 // cannot ask for the bytes fast enough, and joins through distributed shared memory.
 #include <cstdint>
+#include <type_traits>
 #include "common.cuh"
 
 namespace slim {
@@ -118,6 +120,29 @@ __device__ __forceinline__ void lp_unpack(const uint4& q, float (&v)[kVec]) {
   }
 }
 
+// The largest of kCount vectors (a NaN counts as nothing). bf16 pairs are compared as pairs.
+template <typename E, int kCount>
+__device__ __forceinline__ float lp_top(const uint4 (&q)[kCount]) {
+  if constexpr (sizeof(E) == 4) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < kCount; ++b)
+      top = fmaxf(top, fmaxf(fmaxf(__uint_as_float(q[b].x), __uint_as_float(q[b].y)),
+                             fmaxf(__uint_as_float(q[b].z), __uint_as_float(q[b].w))));
+    return top;
+  } else {
+    uint32_t t = 0xFF80FF80u;  // -inf, -inf
+#pragma unroll
+    for (int b = 0; b < kCount; ++b) {
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(t) : "r"(q[b].x));
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(t) : "r"(q[b].y));
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(t) : "r"(q[b].z));
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(t) : "r"(q[b].w));
+    }
+    return fmaxf(__uint_as_float(t << 16), __uint_as_float(t & 0xFFFF0000u));
+  }
+}
+
 template <typename E, int kThreads>
 __global__ void __launch_bounds__(kThreads)
 lp_kernel(const E* __restrict__ logits, int64_t V, int64_t ld, const int64_t* __restrict__ tokens, int top_k,
@@ -126,10 +151,11 @@ lp_kernel(const E* __restrict__ logits, int64_t V, int64_t ld, const int64_t* __
   constexpr int kVec = 16 / sizeof(E), kWarps = kThreads / 32, kBatch = 4;
   __shared__ LpStat s_stat[kWarps];
   __shared__ LpStat s_cta;
-  __shared__ uint64_t s_best[kWarps][32];
+  __shared__ uint64_t s_best[32];
+  __shared__ float s_top[kWarps][32];
   __shared__ uint64_t s_cand[LP_CAND];
   __shared__ uint64_t s_out[LP_MAX_K];
-  __shared__ uint64_t s_bound;
+  __shared__ float s_bound;
   __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x / split;
@@ -157,75 +183,48 @@ lp_kernel(const E* __restrict__ logits, int64_t V, int64_t ld, const int64_t* __
     return LpStat{v == v ? v : -INFINITY, v == INFINITY || v != v ? NAN : (v == -INFINITY ? 0.f : 1.f), 0.f};
   };
   LpStat st = {-INFINITY, 0.f, 0.f};
-  uint32_t first_max = 0;  // the index of the thread's maximum, its first
-  bool any = in_head;
-  if (in_head) {
-    st = single(odd_value);
-    first_max = (uint32_t)odd;
-  }
-  for (uint32_t i = v0 + tid; i < v1; i += kThreads * kBatch) {
-    uint4 q[kBatch];
+  if (odd >= 0) st = single(odd_value);
+  // kBatch vectors, kThreads apart; what is past the part counts as -inf
+  auto take = [&](auto whole, uint32_t i) {
+    constexpr int kCount = kBatch;
+    constexpr uint32_t kNone = sizeof(E) == 4 ? 0xFF800000u : 0xFF80FF80u;
+    uint4 q[kCount];
     float v[kVec];
-    const uint32_t left = (v1 - i + kThreads - 1) / kThreads;
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-      if (b < left) q[b] = __ldg(xv + i + b * kThreads);
-    float top = -INFINITY;
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-      if (b < left) {
-        lp_unpack<E, kVec>(q[b], v);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) top = fmaxf(top, v[j]);
-      }
+    for (int b = 0; b < kCount; ++b)
+      q[b] = decltype(whole)::value || i + b * kThreads < v1 ? __ldg(xv + i + b * kThreads)
+                                                             : make_uint4(kNone, kNone, kNone, kNone);
+    const float top = lp_top<E, kCount>(q);
     if (top > st.m) {
       if (st.m == -INFINITY) st.m = top; else st.rise(top);
-      bool found = false;
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b)
-        if (b < left) {
-          lp_unpack<E, kVec>(q[b], v);
-#pragma unroll
-          for (int j = 0; j < kVec; ++j)
-            if (!found && v[j] == top) {
-              found = true;
-              first_max = head + (i + b * kThreads) * kVec + j;
-            }
-        }
-    } else if (!any) {
-      first_max = head + i * kVec;  // nothing above -inf: the first element stands for the thread
     }
-    any = true;
     const float base = st.m == -INFINITY ? 0.f : -st.m;
     const uint64_t base2 = lp_pair(base, base), l2 = lp_pair(kLog2e, kLog2e);
     uint64_t S2 = 0ull, T2 = 0ull;
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-      if (b < left) {
-        lp_unpack<E, kVec>(q[b], v);
+    for (int b = 0; b < kCount; ++b) {
+      lp_unpack<E, kVec>(q[b], v);
 #pragma unroll
-        for (int j = 0; j < kVec; j += 2) {
-          float d0, d1, e0, e1;
-          lp_unpair(lp_add2(lp_pair(v[j], v[j + 1]), base2), d0, d1);
-          const uint64_t d = lp_pair(lp_max_nan(d0, kFar), lp_max_nan(d1, kFar));
-          lp_unpair(lp_mul2(d, l2), e0, e1);
-          const uint64_t e = lp_pair(lp_ex2(e0), lp_ex2(e1));
-          S2 = lp_add2(S2, e);
-          T2 = lp_fma2(e, d, T2);
-        }
+      for (int j = 0; j < kVec; j += 2) {
+        float d0, d1, e0, e1;
+        lp_unpair(lp_add2(lp_pair(v[j], v[j + 1]), base2), d0, d1);
+        const uint64_t d = lp_pair(lp_max_nan(d0, kFar), lp_max_nan(d1, kFar));
+        lp_unpair(lp_mul2(d, l2), e0, e1);
+        const uint64_t e = lp_pair(lp_ex2(e0), lp_ex2(e1));
+        S2 = lp_add2(S2, e);
+        T2 = lp_fma2(e, d, T2);
       }
+    }
     float a, b;
     lp_unpair(S2, a, b);
     st.S += a + b;
     lp_unpair(T2, a, b);
     st.T += a + b;
-  }
-  if (in_tail) {
-    if (!any || odd_value > st.m) first_max = (uint32_t)odd;
-    st.join(single(odd_value));
-    any = true;
-  }
-  const uint64_t mine = any ? lp_key(st.m, first_max) : 0ull;
+  };
+  uint32_t i0 = v0 + tid;
+  for (; i0 + (kBatch - 1) * kThreads < v1; i0 += kThreads * kBatch) take(std::true_type{}, i0);
+  if (i0 < v1) take(std::false_type{}, i0);
+  const bool any = odd >= 0 || v0 + tid < v1;
 
   // the CTA's statistics, in a fixed order
   LpStat w = st;
@@ -236,7 +235,7 @@ lp_kernel(const E* __restrict__ logits, int64_t V, int64_t ld, const int64_t* __
     w.join(other);
   }
   if (lane == 0) s_stat[warp] = w;
-  if (top_k) s_best[warp][lane] = mine;
+  if (top_k) s_top[warp][lane] = any ? st.m : -INFINITY;
   if (tid == 0) s_count = 0;
   __syncthreads();
   if (warp == 0) {
@@ -249,13 +248,13 @@ lp_kernel(const E* __restrict__ logits, int64_t V, int64_t ld, const int64_t* __
     }
     if (lane == 0) s_cta = c;
     if (top_k) {
-      uint64_t g = 0;
+      float g = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < kWarps; ++u) g = lp_max(g, s_best[u][lane]);
+      for (int u = 0; u < kWarps; ++u) g = fmaxf(g, s_top[u][lane]);
       int above = 0;
 #pragma unroll
       for (int u = 0; u < 32; ++u) {
-        const uint64_t o = __shfl_sync(0xffffffffu, g, u);
+        const float o = __shfl_sync(0xffffffffu, g, u);
         above += o > g || (o == g && u < lane) ? 1 : 0;
       }
       if (above == top_k - 1) s_bound = g;
@@ -263,25 +262,26 @@ lp_kernel(const E* __restrict__ logits, int64_t V, int64_t ld, const int64_t* __
   }
   __syncthreads();
   if (top_k) {
-    const uint64_t bound = s_bound;
+    const float bound = s_bound;
+    const bool masked = bound == -INFINITY;
     bool scan = s_cta.S != s_cta.S;  // a NaN or +inf
     if (!scan) {
-      if (any && mine >= bound) {
-        auto offer = [&](float v, uint32_t idx) {
-          const uint64_t key = lp_key(v, idx);
-          if (key >= bound) {
-            const int at = atomicAdd(&s_count, 1);  // (the order does not matter: keys are ranked)
-            if (at < LP_CAND) s_cand[at] = key;
-          }
-        };
-        if (odd >= 0) offer(odd_value, (uint32_t)odd);
-        for (uint32_t i = v0 + tid; i < v1; i += kThreads) {
-          float v[kVec];
-          lp_unpack<E, kVec>(__ldg(xv + i), v);
-          float top = v[0];
-#pragma unroll
-          for (int j = 1; j < kVec; ++j) top = fmaxf(top, v[j]);
-          if (lp_key(top, 0u) >= bound) {
+      const bool reaches = any && st.m >= bound && st.m > -INFINITY;
+      auto offer = [&](float v, uint32_t idx) {
+        if (masked ? v > bound : v >= bound) {
+          const int at = atomicAdd(&s_count, 1);  // (the order does not matter: keys are ranked)
+          if (at < LP_CAND) s_cand[at] = lp_key(v, idx);
+        }
+      };
+      if (reaches && odd >= 0) offer(odd_value, (uint32_t)odd);
+      // the vectors of each such thread, by its whole warp
+      for (unsigned todo = __ballot_sync(0xffffffffu, reaches); todo; todo &= todo - 1) {
+        const uint32_t owner = warp * 32 + __ffs(todo) - 1;
+        for (uint32_t i = v0 + owner + lane * kThreads; i < v1; i += 32 * kThreads) {
+          const uint4 q[1] = {__ldg(xv + i)};
+          if (lp_top<E, 1>(q) >= bound) {
+            float v[kVec];
+            lp_unpack<E, kVec>(q[0], v);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) offer(v[j], head + i * kVec + j);
           }
@@ -298,6 +298,18 @@ lp_kernel(const E* __restrict__ logits, int64_t V, int64_t ld, const int64_t* __
           int above = 0;
           for (int u = 0; u < count; ++u) above += s_cand[u] > key ? 1 : 0;
           if (above < top_k) s_out[above] = key;
+        }
+        if (masked && warp == 0) {  // the lowest indices of -inf follow; at most `count` others lie before them
+          const int64_t begin = rank == 0 ? 0 : head + (int64_t)v0 * kVec;
+          const int64_t end = rank == split - 1 ? V : head + (int64_t)v1 * kVec;
+          int have = count;
+          for (int64_t i = begin; i < end && have < top_k; i += 32) {
+            const bool gone = i + lane < end && lp_load(x + i + lane) == -INFINITY;
+            const unsigned mask = __ballot_sync(0xffffffffu, gone);
+            const int at = have + __popc(mask & ((1u << lane) - 1));
+            if (gone && at < top_k) s_out[at] = lp_key(-INFINITY, (uint32_t)(i + lane));
+            have += __popc(mask);
+          }
         }
       }
     }
@@ -319,10 +331,10 @@ lp_kernel(const E* __restrict__ logits, int64_t V, int64_t ld, const int64_t* __
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) best = lp_max(best, __shfl_xor_sync(0xffffffffu, best, o));
         __syncthreads();
-        if (lane == 0) s_best[0][warp] = best;
+        if (lane == 0) s_best[warp] = best;
         __syncthreads();
         best = 0;
-        for (int u = 0; u < kWarps; ++u) best = lp_max(best, s_best[0][u]);
+        for (int u = 0; u < kWarps; ++u) best = lp_max(best, s_best[u]);
         if (tid == 0) s_out[r] = best;
         last = best;
       }
@@ -408,13 +420,15 @@ cudaError_t launch_logprobs(const void* logits, int dtype, int64_t N, int64_t V,
                             int top_k, float* logp, float* entropy, float* top_logp, int32_t* top_id, int num_sms,
                             cudaStream_t s) {
   const int64_t bytes = V * (dtype == 0 ? 4 : 2);
-  // a row is split until there are two CTAs an SM, while each part is worth a CTA
+  // A row is split while that gives the last wave company (about six CTAs fit an SM: below four waves of them the
+  // last one costs), and its parts are worth a CTA: 1024 x 100003 fp32 takes 146 us whole and SPLITUS in four.
   int split = 1;
-  while (split < 8 && N * split < 2 * num_sms && bytes / (2 * split) >= 8192) split *= 2;
+  while (split < 8 && N * split < 24 * num_sms && bytes / (2 * split) >= (N * split < 2 * num_sms ? 8192 : 65536))
+    split *= 2;
   const bool small = bytes / split <= 16384;
 #define SLIM_LP(E)                                                                                                    \
   (small ? launch_lp<E, 128>(logits, N, V, ld, tokens, top_k, split, logp, entropy, top_logp, top_id, s)             \
-         : launch_lp<E, 512>(logits, N, V, ld, tokens, top_k, split, logp, entropy, top_logp, top_id, s))
+         : launch_lp<E, 256>(logits, N, V, ld, tokens, top_k, split, logp, entropy, top_logp, top_id, s))
   return dtype == 0 ? SLIM_LP(float) : SLIM_LP(uint16_t);
 #undef SLIM_LP
 }
