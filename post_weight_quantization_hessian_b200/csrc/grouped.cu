@@ -31,9 +31,10 @@ cudaError_t take_async_status(DevStatus* host, cudaStream_t s) {
 // Sums of x over each column group, as the bf16 parts that the correction
 // columns of the tensor-core kernel take (below), and where that kernel cannot
 // read x as it is (gathered rows, fp32), the rows as bf16 in grouped order: fp32
-// as three planes x1 + x2 + x3 that hold all 24 bits. A warp takes a row, with
-// 16-byte loads and stores; bound by the bytes of x (read, and written if copied).
-constexpr int GP_ROWS = 8;
+// as three planes x1 + x2 + x3 that hold all 24 bits. A warp takes 512 columns of
+// a row, with 16-byte loads and stores; bound by the bytes of x (read, and
+// written if copied).
+constexpr int GP_ROWS = 8, GP_COLS = 512;
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -80,7 +81,11 @@ gg_prep_kernel(const void* __restrict__ x, int xdtype, int64_t T, const int32_t*
   const int per = group / 8;  // lanes of a group
   const int64_t src = row_index ? row_index[r] : r;
   const bool have = src >= 0 && src < T;
-  for (int64_t j = lane * 8; j < (n + 255) / 256 * 256; j += 256) {
+  const int64_t j0 = (int64_t)blockIdx.y * GP_COLS;
+#pragma unroll
+  for (int step = 0; step < GP_COLS / 256; ++step) {
+    const int64_t j = j0 + step * 256 + lane * 8;
+    if (j - lane * 8 >= n) break;
     float v[8];
     uint32_t p[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -107,7 +112,7 @@ gg_prep_kernel(const void* __restrict__ x, int xdtype, int64_t T, const int32_t*
     if (xs && lane % per == 0) {
       uint32_t o[kSlots / 2];
       split_slots<kSlots, false>(s, o);
-      uint16_t* dst = xs + r * xs_stride + j / group * kSlots;
+      uint16_t* dst = xs + r * xs_stride + (uint32_t)j / (uint32_t)group * kSlots;
       if constexpr (kSlots == 8)
         *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
       else
@@ -177,13 +182,13 @@ __device__ __forceinline__ int gt_slots(const GtParams& p, int lane, int* s_expe
 }
 
 // ---------------------------------------------------------------- decoding
-// One block: 128 outputs x up to 16 boxes of 64 columns of one slot. A thread
+// One block: 128 outputs x up to 4 boxes of 64 columns of one slot. A thread
 // takes 8 codes (b bytes of the row's stream) and writes the 16 bytes of their
 // bf16 values where the product's shared-memory layout wants them (K-major, 128-
 // byte swizzle), so that a warp writes 512 consecutive bytes and the product
 // loads a whole tile with one bulk copy. Behind the boxes of codes come those of
 // the correction columns. Bound by the bytes written.
-constexpr int GD_THREADS = 256, GD_BOXES = 16;
+constexpr int GD_THREADS = 256, GD_BOXES = 4;
 
 template <int B, bool kCenter>
 __device__ __forceinline__ uint4 decode8(uint32_t lo, uint32_t hi) {
@@ -221,9 +226,9 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
   for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   if (lane == 0) atomicAdd(&s_before, before);  // (integers: the order does not matter)
   __syncthreads();
-  if (tid < 32) {  // lane = unit of the block
+  if (tid < 32) {  // lane = unit of the block (the first may lie inside a group)
     const int unit = kb0 * 2 + lane, c = unit / kUnits;
-    int b = c < p.k ? bits[c] : 0;
+    int b = c < p.k && lane < GD_BOXES * 2 ? bits[c] : 0;
     if (b > 8) b = 0;
     int incl = b;
 #pragma unroll
@@ -233,7 +238,7 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
     }
     const int first = s_before * kUnits + incl - b;
     // widths that do not fill a row: nothing outside it is read
-    s_width[lane] = first + b > p.rw ? 0u : (uint32_t)first << 4 | (uint32_t)b;
+    if (lane < GD_BOXES * 2) s_width[lane] = first + b > p.rw ? 0u : (uint32_t)first << 4 | (uint32_t)b;
   }
   __syncthreads();
   const int chunk = tid & 7, h = chunk >> 2;
@@ -1163,7 +1168,7 @@ cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const flo
   const int k = (int)(n / group);
   cudaError_t e = cudaSuccess;
   if (xs || xg) {
-    const unsigned blocks = (unsigned)((R + GP_ROWS - 1) / GP_ROWS);
+    const dim3 blocks((unsigned)((R + GP_ROWS - 1) / GP_ROWS), (unsigned)((n + GP_COLS - 1) / GP_COLS));
     if (ydtype == 0)
       gg_prep_kernel<8><<<blocks, GP_ROWS * 32, 0, s>>>(x, xdtype, T, row_index, R, n, group, xg, xs, g.xs_stride);
     else
