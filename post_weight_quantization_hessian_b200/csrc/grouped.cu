@@ -312,9 +312,8 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
 // Rows of two neighbouring experts may share an x box: an accumulator column
 // depends on its own row of x alone, and only the tile's rows are stored.
 constexpr int GT_THREADS = 384;
-constexpr int GT_STAGES = 4;
-constexpr int GT_STAGE = GT_ABYTES + GT_XBYTES;
-constexpr int GT_OFF_BAR = GT_STAGES * GT_STAGE;
+constexpr int GT_MAX_STAGES = 8;  // of a ring of 192 KB: 4, 6 or 8 for tiles of 256, 128 or 64 rows
+constexpr int GT_OFF_BAR = 4 * (GT_ABYTES + GT_XBYTES);
 constexpr int GT_OFF_E = GT_OFF_BAR + 256;
 constexpr int GT_SMEM = GT_OFF_E + (2 * GT_MAX_E + 1) * 4 + 1024;  // + alignment
 static_assert(GT_SMEM <= 227 * 1024, "shared memory of a CTA");
@@ -383,15 +382,16 @@ __device__ __forceinline__ bool gt_wait(uint32_t bar, uint32_t parity, volatile 
   return false;
 }
 
-// Tiles of the rows [r0, r1): count, and the width of each.
-__device__ __forceinline__ int gt_row_tiles(int r0, int r1, int& width) {
-  const int span = r1 - r0, nt = (span + GT_N - 1) / GT_N;
+// Tiles of at most `most` of the rows [r0, r1): count, and the width of each.
+__device__ __forceinline__ int gt_row_tiles(int r0, int r1, int most, int& width) {
+  const int span = r1 - r0, nt = (span + most - 1) / most;
   width = nt ? ((span + nt - 1) / nt + 15) & ~15 : 0;
   return nt;
 }
 
 // first[s]: the row tiles of the slots before s, times the output tiles of the pass.
-__device__ __forceinline__ GtTile gt_tile(const GtParams& p, int t, int slots, const int* first, const int* expert) {
+__device__ __forceinline__ GtTile gt_tile(const GtParams& p, int t, int slots, int most, const int* first,
+                                          const int* expert) {
   int lo = 0, hi = slots;  // the last slot whose first tile is <= t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -403,7 +403,7 @@ __device__ __forceinline__ GtTile gt_tile(const GtParams& p, int t, int slots, c
   const int r0 = gt_clamp(p.offsets[u.e], p.R);
   u.r1 = gt_clamp(p.offsets[u.e + 1], p.R);
   int width;
-  gt_row_tiles(r0, u.r1, width);
+  gt_row_tiles(r0, u.r1, most, width);
   const int j = (t - first[lo]) / p.mtn;
   u.mt = t - first[lo] - j * p.mtn;
   u.col0 = r0 + j * width;
@@ -417,8 +417,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + GT_OFF_BAR);
-  uint64_t* empty = full + GT_STAGES;
-  uint64_t* dfull = empty + GT_STAGES;
+  uint64_t* empty = full + GT_MAX_STAGES;
+  uint64_t* dfull = empty + GT_MAX_STAGES;
   uint64_t* dempty = dfull + 2;
   uint64_t* done = dempty + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: the roles' loops run on uniform registers
   if (tid == 0) {
-    for (int i = 0; i < GT_STAGES; ++i) { mbar_init(&full[i], 2); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < GT_MAX_STAGES; ++i) { mbar_init(&full[i], 2); mbar_init(&empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&dfull[i], 1); mbar_init(&dempty[i], 8); }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -442,32 +442,39 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
   if (warp == 0) {  // slots and the tiles before each
     const int slots = gt_slots(p, lane, s_expert);
     __syncwarp();
-    int run = 0;
-    for (int q0 = 0; q0 < slots; q0 += 32) {
-      const int q = q0 + lane;
-      int width, v = 0;
-      if (q < slots) {
-        const int e = s_expert[q];
-        v = gt_row_tiles(gt_clamp(p.offsets[e], p.R), gt_clamp(p.offsets[e + 1], p.R), width) * p.mtn;
-      }
-      int incl = v;
+    // 256 rows a tile, fewer while the tiles would leave SMs idle: a tile's time hardly falls below 64
+    int run = 0, width, most = 2 * GT_N;
+    do {
+      most /= 2;
+      run = 0;
+      for (int q0 = 0; q0 < slots; q0 += 32) {
+        const int q = q0 + lane;
+        int v = 0;
+        if (q < slots) {
+          const int e = s_expert[q];
+          v = gt_row_tiles(gt_clamp(p.offsets[e], p.R), gt_clamp(p.offsets[e + 1], p.R), most, width) * p.mtn;
+        }
+        int incl = v;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += u;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += u;
+        }
+        if (q < slots) s_first[q] = run + incl - v;
+        run += __shfl_sync(0xffffffffu, incl, 31);
       }
-      if (q < slots) s_first[q] = run + incl - v;
-      run += __shfl_sync(0xffffffffu, incl, 31);
-    }
+    } while (most > 64 && run * 2 <= (int)gridDim.x);
     if (lane == 0) {
       s_first[slots] = run;
-      *s_slots = slots;
+      s_slots[0] = slots;
+      s_slots[1] = most;
     }
   }
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tslot;
-  const int slots = *s_slots, tiles = s_first[slots];
+  const int slots = s_slots[0], most = s_slots[1], tiles = s_first[slots];
+  const uint32_t stages = most == 256 ? 4 : (most == 128 ? 6 : 8), stage = GT_ABYTES + most * 128;
   const int nbox = (int)((p.n + GT_K - 1) / GT_K);     // boxes of codes
   const int ncor = (p.k + kCorr - 1) / kCorr;          // boxes of correction columns
 
@@ -478,7 +485,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
     GtRing dr;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const GtTile u = gt_tile(p, t, slots, s_first, s_expert);
+      const GtTile u = gt_tile(p, t, slots, most, s_first, s_expert);
       const int64_t i = (int64_t)(p.mt0 + u.mt) * GT_M + sub + lane;
       const bool row_ok = i < p.m;
       const float* scale = p.scale + ((int64_t)u.e * p.m + (row_ok ? i : p.m - 1)) * p.k;
@@ -563,7 +570,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
       uint32_t issued = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const GtTile u = gt_tile(p, t, slots, s_first, s_expert);
+        const GtTile u = gt_tile(p, t, slots, most, s_first, s_expert);
         const uint8_t* at = p.tiles + ((int64_t)u.slot * p.mtn + u.mt) * (nbox + ncor) * GT_ABYTES;
         const int nr = (u.N + 31) / 32;
         const uint32_t bytes = (u.N > 128 ? GT_XBYTES : nr * 4096) + GT_ABYTES;
@@ -575,7 +582,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
               ok = false;
               break;
             }
-            uint8_t* dst = smem + r.slot * GT_STAGE;
+            uint8_t* dst = smem + r.slot * stage;
             uint64_t* bar = &full[r.slot];
             mbar_arrive_expect_tx(bar, bytes);
             bulk_load(dst, at + (int64_t)kb * GT_ABYTES, GT_ABYTES, bar);
@@ -586,13 +593,13 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
             } else {
               for (int v = 0; v < nr; ++v) tma_load_2d(dst + v * 4096, cor ? &tm.s32 : &tm.x32, bar, x0, y0 + 32 * v);
             }
-            r.step(GT_STAGES);
+            r.step(stages);
           }
         }
       }
       // let every issued copy land before the CTA can exit, also after an abort
-      for (uint32_t j = issued > GT_STAGES ? issued - GT_STAGES : 0; ok == false && j < issued; ++j)
-        mbar_drain(&full[j % GT_STAGES], (j / GT_STAGES) & 1);
+      for (uint32_t j = issued > stages ? issued - stages : 0; !ok && j < issued; ++j)
+        mbar_drain(&full[j % stages], (j / stages) & 1);
     } else if (warp == 10 && lane == 0) {
       // ---------------------------------------------------------- gate
       GtRing r, dr;
@@ -612,7 +619,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
                 dr.step(2);
               }
             if (ok) mbar_arrive(&full[r.slot]);
-            r.step(GT_STAGES);
+            r.step(stages);
           }
         }
       }
@@ -627,7 +634,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
       GtRing r, dr;
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const GtTile u = gt_tile(p, t, slots, s_first, s_expert);
+        const GtTile u = gt_tile(p, t, slots, most, s_first, s_expert);
         const uint32_t idesc = idesc_bf16_f32(GT_M, 16, false, false) + ((uint32_t)(u.N / 8 - 2) << 17);
         // kPer: boxes of a group (0: all n boxes are one); kParts: groups of a box
         auto boxes = [&](auto per_group, int n, int planes) {
@@ -640,7 +647,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
             for (int q = 0; q < planes; ++q) {
               if (!gt_wait(smem_u32(full) + 8 * r.slot, r.phase, abort_flag, 40)) return false;
               tc_fence_after();
-              const uint64_t ad = kDesc + (a0 + r.slot * (GT_STAGE / 16)), bd = ad + GT_ABYTES / 16;
+              const uint64_t ad = kDesc + (a0 + r.slot * (stage / 16)), bd = ad + GT_ABYTES / 16;
               if (lead) {
 #pragma unroll
                 for (int k16 = 0; k16 < 4; ++k16)
@@ -649,7 +656,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
                 tc_commit(&empty[r.slot]);
                 if (ends && q == planes - 1) tc_commit(&dfull[dr.slot]);
               }
-              r.step(GT_STAGES);
+              r.step(stages);
             }
             if (ends) dr.step(2);
           }
@@ -670,13 +677,13 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
               for (int q = 0; q < planes; ++q) {
                 if (h == 0 && !gt_wait(smem_u32(full) + 8 * rs.slot, rs.phase, abort_flag, 42)) return false;
                 tc_fence_after();
-                const uint64_t ad = kDesc + (a0 + rs.slot * (GT_STAGE / 16) + 4 * h), bd = ad + GT_ABYTES / 16;
+                const uint64_t ad = kDesc + (a0 + rs.slot * (stage / 16) + 4 * h), bd = ad + GT_ABYTES / 16;
                 if (lead) {
                   tc_mma_bf16(tbase + dr.slot * GT_N, ad, bd, idesc, q == 0 ? 0u : 1u);
                   tc_mma_bf16(tbase + dr.slot * GT_N, ad + 2, bd + 2, idesc, 1u);
                   if (h == parts - 1) tc_commit(&empty[rs.slot]);
                 }
-                rs.step(GT_STAGES);
+                rs.step(stages);
               }
               if (lead) tc_commit(&dfull[dr.slot]);
               dr.step(2);
@@ -717,16 +724,16 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
 // next to HBM, not the tensor work, so the warp-level instruction fits: no
 // operand passes through shared or tensor memory.
 //
-// A CTA of 4 warps takes 128 outputs (a warp 32) and a range of 256-column
-// chunks; the CTAs of a cluster share the outputs and split the depth, and add
+// A CTA of 8 warps takes 128 outputs and a range of 256-column chunks; a warp
+// takes 32 of the outputs and every other group; the CTAs of a cluster share the outputs and split the depth, and add
 // their sums through distributed shared memory in a fixed order. Codes and x
 // arrive by asynchronous copies, two chunks ahead; scales and zeros go through
 // registers one chunk ahead. Of 64 columns (32 in groups of 32) thread (g, t) of a
 // warp takes the 16 (8) codes from 16 t (8 t) on of rows g, g + 8, g + 16, g + 24:
 // as k-steps may take the columns in any order that x follows, those are its
-// pairs of four (two) k-steps, and x's are consecutive bytes. The group sums of
-// x are the product with a row of ones.
-constexpr int GS_THREADS = 128, GS_M = 128, GS_K = 256, GS_STAGES = 2;
+// pairs of four (two) k-steps, and x's are consecutive bytes. The sums of x over
+// 32 columns are products with rows of ones, a unit of the chunk for each warp.
+constexpr int GS_THREADS = 256, GS_M = 128, GS_K = 256, GS_STAGES = 2;
 // Bytes of a row of x: the 16-byte reads of two rows and four threads meet no bank twice.
 __host__ __device__ constexpr int gs_xstride(int group) { return GS_K * 2 + (group == 32 ? 64 : 16); }
 
@@ -762,7 +769,7 @@ __device__ __forceinline__ void gs_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
 
 // kNT: tiles of 8 rows at a time; kPlanes: bf16 planes of x.
 template <int G, bool kCenter, int kNT, int kPlanes>
-__global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
+__global__ void __launch_bounds__(GS_THREADS, kNT == 1 ? 3 : 2) gs_kernel(const GsParams p) {
   constexpr int kUnits = G / 32, kGroups = GS_K / G, kRows = 8 * kNT;
   constexpr int kSub = G == 32 ? 32 : 64, kCodes = kSub / 4;  // columns decoded at a time, and a thread's of a row
   constexpr int GS_XSTRIDE = gs_xstride(G);
@@ -771,7 +778,9 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
   __shared__ uint32_t s_width[1024];               // first word << 4 | width of each group
   __shared__ float2 s_coef[2][kGroups][GS_M];      // coef_d, coef_x
   __shared__ int s_row[kRows];                     // row of x, -1: zeros
+  __shared__ float2 s_sum[GS_K / 32][kRows / 2];   // sums of x over 32 columns, of two rows
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  const int out0 = (warp & 3) * 32, part = warp >> 2;  // the warp's outputs, and which of the chunk's groups
   const int rank = blockIdx.x % p.split, mt = blockIdx.x / p.split;
   // the expert of this slot among those with 1 .. few_rows rows
   if (warp == 0) {
@@ -820,7 +829,10 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
   const uint32_t sbase = smem_u32(gs_smem);
   const uint32_t xbytes = kPlanes * kRows * GS_XSTRIDE, stage = xbytes + GS_M * p.wstride * 4;
   const bool wide = (p.rw & 3) == 0;  // rows of 16-byte multiples
-  const int64_t srow = (base + m0 + min(tid, mrows - 1)) * p.k;  // this thread's scales and zeros
+  // this thread's scales and zeros: an output's, of one half of a chunk's groups
+  const int64_t srow = (base + m0 + min(tid & (GS_M - 1), mrows - 1)) * p.k;
+  constexpr int kHalf = kGroups / 2;
+  const int chalf = (tid / GS_M) * kHalf;
 
   // words [first, end) of a chunk
   auto chunk_words = [&](int ch, int& first, int& end) {
@@ -866,16 +878,17 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
         int first, end;
         chunk_words(ch, first, end);
         end = min(end, first + p.cap);
-        const int row = tid >> 3;  // and every 16th from it
-        const uint32_t rstep = 16 * p.wstride * 4;
+        const int row = tid >> 3;  // and every 32nd from it
+        constexpr int kStep = GS_THREADS / 8;
+        const uint32_t rstep = kStep * p.wstride * 4;
         if (wide) {
           for (int w = (tid & 7) * 4; w < end - first; w += 32) {
             const uint32_t* src = codes0 + first + w;
             uint32_t dst = sw + (row * p.wstride + w) * 4;
 #pragma unroll
-            for (int i = 0; i < GS_M / 16; ++i) {
-              if (row + 16 * i < mrows) gs_cp16(dst, src, 16u);
-              src += 16 * p.rw;
+            for (int i = 0; i < GS_M / kStep; ++i) {
+              if (row + kStep * i < mrows) gs_cp16(dst, src, 16u);
+              src += kStep * p.rw;
               dst += rstep;
             }
           }
@@ -884,9 +897,9 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
             const uint32_t* src = codes0 + first + w;
             uint32_t dst = sw + (row * p.wstride + w) * 4;
 #pragma unroll
-            for (int i = 0; i < GS_M / 16; ++i) {
-              if (row + 16 * i < mrows) gs_cp4(dst, src);
-              src += 16 * p.rw;
+            for (int i = 0; i < GS_M / kStep; ++i) {
+              if (row + kStep * i < mrows) gs_cp4(dst, src);
+              src += kStep * p.rw;
               dst += rstep;
             }
           }
@@ -894,11 +907,11 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    float sreg[kGroups], zreg[kGroups];
+    float sreg[kHalf], zreg[kHalf];
     auto load_scales = [&](int ch) {
 #pragma unroll
-      for (int c = 0; c < kGroups; ++c) {
-        const int at = min(ch * kGroups + c, p.k - 1);
+      for (int c = 0; c < kHalf; ++c) {
+        const int at = min(ch * kGroups + chalf + c, p.k - 1);
         sreg[c] = __ldg(p.scale + srow + at);
         zreg[c] = __ldg(p.zero + srow + at);
       }
@@ -910,10 +923,10 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
     for (int ch = ch0; ch < ch1; ++ch) {
       // coefficients of this chunk (their buffer was last read two chunks ago)
 #pragma unroll
-      for (int c = 0; c < kGroups; ++c) {
-        const int at = ch * kGroups + c, b = at < p.k ? s_width[at] & 15 : 0;
-        s_coef[ch & 1][c][tid] = b ? make_float2(coef_d<kCenter>(b, sreg[c]), coef_x<kCenter>(b, sreg[c], zreg[c]))
-                                   : make_float2(0.f, 0.f);
+      for (int c = 0; c < kHalf; ++c) {
+        const int at = ch * kGroups + chalf + c, b = at < p.k ? s_width[at] & 15 : 0;
+        s_coef[ch & 1][chalf + c][tid & (GS_M - 1)] =
+            b ? make_float2(coef_d<kCenter>(b, sreg[c]), coef_x<kCenter>(b, sreg[c], zreg[c])) : make_float2(0.f, 0.f);
       }
       if (ch + 1 < ch1) load_scales(ch + 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(GS_STAGES - 2) : "memory");
@@ -922,18 +935,35 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
       int first, end;
       chunk_words(ch, first, end);
       const uint32_t sx = sbase + slot * stage + g * GS_XSTRIDE + t4 * kCodes * 2;
-      const uint32_t sw = sbase + slot * stage + xbytes + (warp * 32 + g) * p.wstride * 4;
+      const uint32_t sw = sbase + slot * stage + xbytes + (out0 + g) * p.wstride * 4;
+      // the sums of x over the warp's unit of 32 columns (rows of ones: every row of the product is the sum)
+#pragma unroll
+      for (int q = 0; q < kNT; ++q)
+        if (q < nt) {
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int pl = kPlanes - 1; pl >= 0; --pl) {
+            uint32_t b0, b1, b2, b3;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
+                         : "r"(sbase + slot * stage + (pl * kRows + q * 8 + g) * GS_XSTRIDE + warp * 64 + t4 * 16));
+            gs_mma(sum, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, b0, b1);
+            gs_mma(sum, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, b2, b3);
+          }
+          if (g == 0) s_sum[warp][q * 4 + t4] = make_float2(sum[0], sum[1]);
+        }
+      __syncthreads();
       const bool fits = end - first <= p.cap;
 #pragma unroll 1
-      for (int c = 0; c < kGroups; ++c) {
+      for (int c = part; c < kGroups; c += 2) {
         if (ch * kGroups + c >= p.k) break;
         const uint32_t en = s_width[ch * kGroups + c], b = en & 15;
         if (b == 0) continue;  // not a width
-        float d[2][kNT][4], xs[kNT][4];
+        float d[2][kNT][4];
 #pragma unroll
         for (int q = 0; q < kNT; ++q)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) d[0][q][v] = d[1][q][v] = xs[q][v] = 0.f;
+          for (int v = 0; v < 4; ++v) d[0][q][v] = d[1][q][v] = 0.f;
         const uint32_t wrel = (en >> 4) - first;
 #pragma unroll 1
         for (int u = 0; u < G / kSub; ++u) {
@@ -955,7 +985,7 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
         _Pragma("unroll") for (int q = 0; q < kWords + (kMore ? 1 : 0); ++q)                                  \
             asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[q]) : "r"(at + 4 * q));                           \
       } else { /* wider than the stage was made for: straight from global memory */                           \
-        const int row = min(warp * 32 + g + 8 * r, mrows - 1);                                                \
+        const int row = min(out0 + g + 8 * r, mrows - 1);                                                     \
         const uint32_t* src = p.codes + (base + m0 + row) * p.rw;                                             \
         _Pragma("unroll") for (int q = 0; q < kWords + (kMore ? 1 : 0); ++q) {                                \
           const int64_t at = first + (bit >> 5) + q;                                                          \
@@ -989,22 +1019,30 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
                     gs_mma(d[a][q], A[2 * a][4 * h + 2], A[2 * a + 1][4 * h + 2], A[2 * a][4 * h + 3],
                            A[2 * a + 1][4 * h + 3], b2, b3);
                   }
-                  gs_mma(xs[q], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, b0, b1);
-                  gs_mma(xs[q], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, b2, b3);
                 }
               }
         }
+        float2 co[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float2 co = s_coef[ch & 1][c][warp * 32 + g + 8 * r];
+        for (int r = 0; r < 4; ++r) co[r] = s_coef[ch & 1][c][out0 + g + 8 * r];
 #pragma unroll
-          for (int q = 0; q < kNT; ++q)
+        for (int q = 0; q < kNT; ++q)
+          if (q < nt) {
+            float2 xs = s_sum[c * kUnits][q * 4 + t4];
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              float& to = acc[r >> 1][q][(r & 1) * 2 + v];
-              to = fmaf(co.x, d[r >> 1][q][(r & 1) * 2 + v], fmaf(co.y, xs[q][v], to));
+            for (int u = 1; u < kUnits; ++u) {
+              const float2 more = s_sum[c * kUnits + u][q * 4 + t4];
+              xs.x += more.x;
+              xs.y += more.y;
             }
-        }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              float* to = &acc[r >> 1][q][(r & 1) * 2];
+              const float* dd = &d[r >> 1][q][(r & 1) * 2];
+              to[0] = fmaf(co[r].x, dd[0], fmaf(co[r].y, xs.x, to[0]));
+              to[1] = fmaf(co[r].x, dd[1], fmaf(co[r].y, xs.y, to[1]));
+            }
+          }
       }
       slot = slot == GS_STAGES - 1 ? 0 : slot + 1;
     }
@@ -1013,12 +1051,21 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
     // the CTA's sums [row of x][output], then the cluster's in rank order
     float* red = reinterpret_cast<float*>(gs_smem);
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+    for (int turn = 1; turn >= 0; --turn) {  // the second half of the groups, then the first on top
+      if (part == turn) {
 #pragma unroll
-      for (int q = 0; q < kNT; ++q)
+        for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-          if (q < nt) red[(q * 8 + t4 * 2 + (v & 1)) * GS_M + warp * 32 + a * 16 + g + (v >> 1) * 8] = acc[a][q][v];
+          for (int q = 0; q < kNT; ++q)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (q < nt) {
+                float* to = &red[(q * 8 + t4 * 2 + (v & 1)) * GS_M + out0 + a * 16 + g + (v >> 1) * 8];
+                *to = turn ? acc[a][q][v] : *to + acc[a][q][v];
+              }
+      }
+      if (turn) __syncthreads();
+    }
     if (p.split > 1) {
       asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -1057,7 +1104,7 @@ __global__ void __launch_bounds__(GS_THREADS) gs_kernel(const GsParams p) {
 
 // ---------------------------------------------------------------- host side
 constexpr int kFewRows = 64;  // experts with at most this many rows: the few-rows kernel
-constexpr size_t kTileBytes = size_t(64) << 20;  // decoded tiles of a pass: they stay in L2 (126 MB)
+constexpr size_t kTileBytes = size_t(1) << 30;  // decoded tiles of a pass
 
 struct GroupedPlan {
   int planes;          // bf16 planes copied in grouped order (0: x is read as it is)
@@ -1126,10 +1173,10 @@ static cudaError_t launch_few(GsParams p, int64_t slots, int avg_bits, int num_s
   p.cap = GS_K / 32 * std::min(avg_bits + 1, 8) + 4;
   p.wstride = (p.cap + 7) / 8 * 8 + 4;  // 4 modulo 8: the eight rows of a read meet no bank twice
   const size_t smem = (size_t)GS_STAGES * (kPlanes * 8 * kNT * gs_xstride(G) + GS_M * p.wstride * 4);
-  // the depth is split over a cluster until about four CTAs an SM have work
+  // the depth is split over a cluster until about three CTAs an SM have work
   const int64_t tiles = slots * p.mtiles, chunks = (p.n + GS_K - 1) / GS_K;
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= (int64_t)num_sms * 6 && chunks >= split * 2) split *= 2;
+  while (split < 8 && tiles * split * 2 <= (int64_t)num_sms * 4 && chunks >= split * 2) split *= 2;
   p.split = split;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.mtiles * split), (unsigned)slots, 1);
