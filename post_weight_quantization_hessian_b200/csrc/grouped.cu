@@ -769,13 +769,14 @@ __device__ __forceinline__ void gs_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
 
 // kNT: tiles of 8 rows at a time; kPlanes: bf16 planes of x.
 template <int G, bool kCenter, int kNT, int kPlanes>
-__global__ void __launch_bounds__(GS_THREADS, kNT == 1 ? 3 : 2) gs_kernel(const GsParams p) {
+__global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
   constexpr int kUnits = G / 32, kGroups = GS_K / G, kRows = 8 * kNT;
   constexpr int kSub = G == 32 ? 32 : 64, kCodes = kSub / 4;  // columns decoded at a time, and a thread's of a row
   constexpr int GS_XSTRIDE = gs_xstride(G);
   extern __shared__ __align__(16) uint8_t gs_smem[];
   __shared__ int s_expert, s_found;
   __shared__ uint32_t s_width[1024];               // first word << 4 | width of each group
+  __shared__ int2 s_words[1024 * 32 / GS_K];       // first and last word of each chunk
   __shared__ float2 s_coef[2][kGroups][GS_M];      // coef_d, coef_x
   __shared__ int s_row[kRows];                     // row of x, -1: zeros
   __shared__ float2 s_sum[GS_K / 32][kRows / 2];   // sums of x over 32 columns, of two rows
@@ -823,26 +824,23 @@ __global__ void __launch_bounds__(GS_THREADS, kNT == 1 ? 3 : 2) gs_kernel(const 
   }
   __syncthreads();
   const int chunks = (int)((p.n + GS_K - 1) / GS_K);
+  const bool wide = (p.rw & 3) == 0;  // rows of 16-byte multiples
+  for (int ch = tid; ch < chunks; ch += GS_THREADS) {  // words [first, end) of each chunk
+    const uint32_t a = s_width[ch * kGroups], z = s_width[min((ch + 1) * kGroups, p.k) - 1];
+    const int first = min((int)(a >> 4), (int)p.rw), end = min((int)(z >> 4) + (int)(z & 15) * kUnits, (int)p.rw);
+    s_words[ch] = make_int2(wide ? first & ~3 : first, end);
+  }
+  __syncthreads();
   const int ch0 = chunks * rank / p.split, ch1 = chunks * (rank + 1) / p.split;
   const int64_t m0 = (int64_t)mt * GS_M, base = (int64_t)e * p.m;
   const int mrows = (int)min((int64_t)GS_M, p.m - m0);
   const uint32_t sbase = smem_u32(gs_smem);
   const uint32_t xbytes = kPlanes * kRows * GS_XSTRIDE, stage = xbytes + GS_M * p.wstride * 4;
-  const bool wide = (p.rw & 3) == 0;  // rows of 16-byte multiples
   // this thread's scales and zeros: an output's, of one half of a chunk's groups
   const int64_t srow = (base + m0 + min(tid & (GS_M - 1), mrows - 1)) * p.k;
   constexpr int kHalf = kGroups / 2;
   const int chalf = (tid / GS_M) * kHalf;
 
-  // words [first, end) of a chunk
-  auto chunk_words = [&](int ch, int& first, int& end) {
-    const int c0 = ch * kGroups, c1 = min(c0 + kGroups, p.k) - 1;
-    first = (int)(s_width[c0] >> 4);
-    end = (int)(s_width[c1] >> 4) + (int)(s_width[c1] & 15) * kUnits;
-    first = min(first, (int)p.rw);
-    end = min(end, (int)p.rw);
-    if (wide) first &= ~3;
-  };
   for (int q0 = r0; q0 < r1; q0 += kRows) {
     const int rows = min(kRows, r1 - q0), nt = (rows + 7) / 8;
     float acc[2][kNT][4];
@@ -875,9 +873,7 @@ __global__ void __launch_bounds__(GS_THREADS, kNT == 1 ? 3 : 2) gs_kernel(const 
                     static_cast<const uint16_t*>(p.x) + pl * p.plane + (have ? src * p.n + ch * GS_K + c * 8 : 0),
                     have ? 16u : 0u);  // 0: zeros
           }
-        int first, end;
-        chunk_words(ch, first, end);
-        end = min(end, first + p.cap);
+        const int first = s_words[ch].x, end = min(s_words[ch].y, first + p.cap);
         const int row = tid >> 3;  // and every 32nd from it
         constexpr int kStep = GS_THREADS / 8;
         const uint32_t rstep = kStep * p.wstride * 4;
@@ -932,8 +928,7 @@ __global__ void __launch_bounds__(GS_THREADS, kNT == 1 ? 3 : 2) gs_kernel(const 
       asm volatile("cp.async.wait_group %0;" ::"n"(GS_STAGES - 2) : "memory");
       __syncthreads();  // this chunk has arrived for all; the slot of the last one is free
       copy_chunk(ch + GS_STAGES - 1, slot == 0 ? GS_STAGES - 1 : slot - 1);
-      int first, end;
-      chunk_words(ch, first, end);
+      const int first = s_words[ch].x;
       const uint32_t sx = sbase + slot * stage + g * GS_XSTRIDE + t4 * kCodes * 2;
       const uint32_t sw = sbase + slot * stage + xbytes + (out0 + g) * p.wstride * 4;
       // the sums of x over the warp's unit of 32 columns (rows of ones: every row of the product is the sum)
@@ -953,7 +948,7 @@ __global__ void __launch_bounds__(GS_THREADS, kNT == 1 ? 3 : 2) gs_kernel(const 
           if (g == 0) s_sum[warp][q * 4 + t4] = make_float2(sum[0], sum[1]);
         }
       __syncthreads();
-      const bool fits = end - first <= p.cap;
+      const bool fits = s_words[ch].y - first <= p.cap;
 #pragma unroll 1
       for (int c = part; c < kGroups; c += 2) {
         if (ch * kGroups + c >= p.k) break;
