@@ -105,10 +105,13 @@ int device_sms(int* sms) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) { g_last_cuda_error = cudaGetErrorString(e); return SLIM_ENODEV; }
+  static std::atomic<int> known[64];  // SM counts of the devices that passed
+  if (dev >= 0 && dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return SLIM_OK;
   int major = 0;
   cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   if (major != 10) return SLIM_ENODEV;
   cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (dev >= 0 && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
   return SLIM_OK;
 }
 

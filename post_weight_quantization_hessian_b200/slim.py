@@ -328,34 +328,38 @@ def slim_dequant_gemv(codes: torch.Tensor, bits: torch.Tensor, scale: torch.Tens
     return y
 
 
+# the current stream's handle without a Stream object around it (2 us of a call of 15)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 _DTYPES = {torch.float32: SLIM_X_F32, torch.bfloat16: SLIM_X_BF16}
 
 
 class _on:
     """The device of the tensors current, and new tensors allocated for the stream that the call runs on."""
 
+    __slots__ = ("guards", "raw")
+
     def __init__(self, device, stream):
-        self.guards = []
-        if device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
+        self.guards = ()
+        if stream is None and device.index == torch.cuda.current_device():  # the usual call: nothing to change
+            self.raw = _raw_stream(device.index)
+            return
+        self.guards = [torch.cuda.device(device)]
+        if stream is None:
+            self.raw = torch.cuda.current_stream(device).cuda_stream
+        else:
             s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
             self.guards.append(torch.cuda.stream(s))
-        self.device = device
+            self.raw = s.cuda_stream
 
     def __enter__(self):
         for g in self.guards:
             g.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return self.raw
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
-
-
-def _need(ok, what: str):
-    if not ok:
-        raise ValueError(what)
 
 
 def slim_dequant_grouped_gemm(codes: torch.Tensor, bits: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor,
@@ -365,28 +369,36 @@ def slim_dequant_grouped_gemm(codes: torch.Tensor, bits: torch.Tensor, scale: to
     """Y_e = X_e W_hat_e^T for packed layers codes [E, m, words], bits [E, k], scale and zero [E, m, k];
     expert e takes the rows offsets[e]..offsets[e + 1] of x [T, n], or with row_index [R] those rows
     of it. y is [R, m], of y_dtype (x's by default); rows of no expert are left as they are."""
+    if scale.dim() != 3 or x.dim() != 2:
+        raise ValueError("scale must be [E, m, k] and x [T, n]")
     E, m, k = scale.shape
     n = k * group
     dev = x.device
-    R = x.shape[0] if row_index is None else row_index.shape[0]
-    _need(x.dim() == 2 and x.shape[1] == n and x.dtype in _DTYPES, "x must be [T, n], bf16 or float32")
-    _need(codes.shape == (E, m, n * avg_bits // 32) and codes.dtype in (torch.int32, torch.uint32),
-          "codes must be [E, m, n * avg_bits / 32] int32")
-    _need(bits.shape == (E, k) and bits.dtype == torch.uint8, "bits must be [E, k] uint8")
-    _need(zero.shape == scale.shape and scale.dtype == zero.dtype == torch.float32,
-          "scale and zero must be [E, m, k] float32")
-    _need(offsets.shape == (E + 1,) and offsets.dtype == torch.int32, "offsets must be [E + 1] int32")
-    _need(row_index is None or (row_index.dim() == 1 and row_index.dtype == torch.int32),
-          "row_index must be [R] int32")
+    T, xn = x.shape
+    R = T if row_index is None else row_index.numel()
+    if xn != n or x.dtype not in _DTYPES:
+        raise ValueError("x must be [T, n], bf16 or float32")
+    if codes.shape != (E, m, n * avg_bits // 32) or codes.dtype not in (torch.int32, torch.uint32):
+        raise ValueError("codes must be [E, m, n * avg_bits / 32] int32")
+    if bits.shape != (E, k) or bits.dtype != torch.uint8:
+        raise ValueError("bits must be [E, k] uint8")
+    if zero.shape != scale.shape or scale.dtype != torch.float32 or zero.dtype != torch.float32:
+        raise ValueError("scale and zero must be [E, m, k] float32")
+    if offsets.shape != (E + 1,) or offsets.dtype != torch.int32:
+        raise ValueError("offsets must be [E + 1] int32")
+    if row_index is not None and (row_index.dim() != 1 or row_index.dtype != torch.int32):
+        raise ValueError("row_index must be [R] int32")
     if y is not None:
-        _need(y.shape == (R, m) and y.dtype in _DTYPES and y_dtype in (None, y.dtype),
-              "y must be [R, m], bf16 or float32")
+        if y.shape != (R, m) or y.dtype not in _DTYPES or y_dtype not in (None, y.dtype):
+            raise ValueError("y must be [R, m], bf16 or float32")
     else:
         y_dtype = x.dtype if y_dtype is None else y_dtype
-        _need(y_dtype in _DTYPES, "y must be [R, m], bf16 or float32")
-    for t in (codes, bits, scale, zero, offsets, row_index, y, ws):
-        _need(t is None or t.device == dev, "all tensors must be on x's device")
-    _need(dev.type == "cuda", "tensors must be on a CUDA device")
+        if y_dtype not in _DTYPES:
+            raise ValueError("y must be [R, m], bf16 or float32")
+    if not (x.is_cuda and codes.device == bits.device == scale.device == zero.device == offsets.device == dev
+            and (row_index is None or row_index.device == dev) and (y is None or y.device == dev)
+            and (ws is None or ws.device == dev)):
+        raise ValueError("all tensors must be on one CUDA device")
     lib = _lib()
     with _on(dev, stream) as s:
         if y is None:
@@ -415,15 +427,22 @@ def slim_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = N
     """(logp, entropy, top_logp, top_id) of logits [N, V] (rows may be strided): the log probability of
     tokens [N] int64 (None without tokens; 0 where a token is outside [0, V)), the entropy, and the
     top_k largest log probabilities with their indices (None when top_k is 0)."""
-    _need(logits.dim() == 2 and logits.dtype in _DTYPES, "logits must be [N, V], bf16 or float32")
+    if logits.dim() != 2 or logits.dtype not in _DTYPES:
+        raise ValueError("logits must be [N, V], bf16 or float32")
     N, V = logits.shape
     dev = logits.device
-    ld = logits.stride(0) if N > 1 else V
-    _need(V >= 1 and (V == 1 or logits.stride(1) == 1) and ld >= V, "the rows of logits must be contiguous")
-    _need(tokens is None or (tokens.shape == (N,) and tokens.dtype == torch.int64 and tokens.device == dev
-                             and tokens.is_contiguous()), "tokens must be [N] int64 on the logits' device")
-    _need(0 <= top_k <= min(32, V), "top_k must be in 0..32 and at most V")
-    _need(dev.type == "cuda", "logits must be on a CUDA device")
+    ld, step = logits.stride()
+    if N <= 1:
+        ld = V
+    if V < 1 or (step != 1 and V > 1) or ld < V:
+        raise ValueError("the rows of logits must be contiguous")
+    if tokens is not None and (tokens.shape != (N,) or tokens.dtype != torch.int64 or tokens.device != dev
+                               or not tokens.is_contiguous()):
+        raise ValueError("tokens must be [N] int64 on the logits' device")
+    if not 0 <= top_k <= 32 or top_k > V:
+        raise ValueError("top_k must be in 0..32 and at most V")
+    if not logits.is_cuda:
+        raise ValueError("logits must be on a CUDA device")
     with _on(dev, stream) as s:
         logp = None if tokens is None else torch.empty(N, dtype=torch.float32, device=dev)
         entropy = torch.empty(N, dtype=torch.float32, device=dev)
