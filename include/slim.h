@@ -339,7 +339,7 @@ int slim_dequant_gemv(const uint32_t* codes, const uint8_t* bits, const float* s
  *            element.
  * 1 <= E <= 1024, E m < 2^31, 0 <= R <= 2^29, 0 <= T < 2^31; R = 0 does nothing. Sums are fp32 or better and
  * in a fixed order: the same inputs give the same y. Products take exact
- * codes; fp32 x enters as three bf16 parts (all 24 bits). The call is
+ * codes; fp32 x enters as three bf16 parts (all 24 bits; |x| up to 3.38e38). The call is
  * asynchronous and can be captured into a CUDA graph; ws must then stay the
  * graph's own. A device-side failure is reported by slim_async_status.
  * Workspace: slim_dequant_grouped_gemm_workspace_bytes (it may be 0; gathered:

@@ -7,10 +7,11 @@
 // ones, and one byte permutation puts the low halves of both side by side. The
 // pairs of a half then differ by a shift alone.
 //
-// With kCenter the value is moved to q 2^-b - 1/2 (exact, one bf16x2 addition):
-// the products' sums then stay near the size of the weights' own share instead
-// of 1.5 sum x, which fp32 outputs need (an error of the fp32 accumulation of
-// about 6e-7 of y without it, 2e-7 with it, at groups of 128).
+// With kCenter the value is moved to q 2^-b - 1/2 (exact, one bf16x2 addition).
+// Without it a group's sum carries about 1.5 sum x, several times the group's own
+// share of the result, and its fp32 roundings with it: far below half a step of
+// a bf16 result, but not of an fp32 one. So fp32 results take the addition (their
+// error against 64 bits is 1e-7 to 4e-7 of their norm).
 // 8-bit codes do not fit the mantissa; they become q - 128, exact in bf16.
 //
 // What a group of width b, scale s and zero z then adds, with D = sum x v and

@@ -138,8 +138,9 @@ gg_prep_kernel(const void* __restrict__ x, int xdtype, int64_t T, const int32_t*
 // ---------------------------------------------------------------- many rows
 // Experts with more than kFewRows rows: their codes are decoded once into bf16
 // tiles in the workspace (gd_kernel), and a tensor-core kernel (gg_tc_kernel)
-// multiplies the tiles with x. The tiles of one pass over the outputs are kept
-// small enough for L2.
+// multiplies the tiles with x, in passes over the outputs that bound the
+// workspace. (Passes whose tiles stay in L2, 64 MB, cost more in their last waves
+// than they saved: 1690 us against 1256 on 8192 rows over eight 11008 x 4096 experts.)
 // (A kernel that decoded each tile inside the product loop was built first: 265 us
 // on 4096 rows of a 4096 x 4096 layer, bound by the decoding warps and the
 // barriers between the roles, a wait of 150 cycles each; every 256 rows decoded
@@ -187,7 +188,9 @@ __device__ __forceinline__ int gt_slots(const GtParams& p, int lane, int* s_expe
 // bf16 values where the product's shared-memory layout wants them (K-major, 128-
 // byte swizzle), so that a warp writes 512 consecutive bytes and the product
 // loads a whole tile with one bulk copy. Behind the boxes of codes come those of
-// the correction columns. Bound by the bytes written.
+// the correction columns. Bound by the bytes written (2 a weight: 14 us for a 4096 x
+// 4096 layer, 171 us for eight of 11008 x 4096, 4.3 TB/s) and by the latency of the
+// codes' loads where there are few blocks.
 constexpr int GD_THREADS = 256, GD_BOXES = 4;
 
 template <int B, bool kCenter>
@@ -311,6 +314,10 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
 // bounds groups of 64 and 32.
 // Rows of two neighbouring experts may share an x box: an accumulator column
 // depends on its own row of x alone, and only the tile's rows are stored.
+// 136 us on 4096 rows of a 4096 x 4096 layer at groups of 128 (1010 TFLOP/s), 1058 us
+// on 8192 rows over eight 11008 x 4096 experts at groups of 64 (698): what bounds it is
+// the chain of an accumulator's hand-over (commit, wait, loads and additions,
+// wait), about 1000 cycles a group besides the 256 to 1024 of its products.
 constexpr int GT_THREADS = 384;
 constexpr int GT_MAX_STAGES = 8;  // of a ring of 192 KB: 4, 6 or 8 for tiles of 256, 128 or 64 rows
 constexpr int GT_OFF_BAR = 4 * (GT_ABYTES + GT_XBYTES);
@@ -748,7 +755,7 @@ struct GsParams {
   void* y;
   int64_t m, n, R, rw, plane;  // plane: values between two planes of x
   int64_t T;
-  int E, k, ydtype, few_rows, mtiles, split;
+  int E, k, few_rows, mtiles, split;
   int cap, wstride;          // code words of a row in a stage, and their stride
 };
 
@@ -1227,7 +1234,7 @@ cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const flo
   f.x = xg ? static_cast<const void*>(xg) : x;
   f.row_index = xg ? nullptr : row_index;
   f.T = xg ? R : T; f.plane = R * n;
-  f.m = m; f.n = n; f.R = R; f.rw = rw; f.E = (int)E; f.k = k; f.ydtype = ydtype; f.few_rows = kFewRows;
+  f.m = m; f.n = n; f.R = R; f.rw = rw; f.E = (int)E; f.k = k; f.few_rows = kFewRows;
   f.mtiles = (int)((m + GS_M - 1) / GS_M);
   const int planes = xdtype == 0 ? 3 : 1;
   const int64_t few = std::min<int64_t>(E, R);
