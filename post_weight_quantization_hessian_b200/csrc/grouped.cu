@@ -1105,7 +1105,10 @@ __global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
 }
 
 // ---------------------------------------------------------------- host side
-constexpr int kFewRows = 64;  // experts with at most this many rows: the few-rows kernel
+// Experts with at most this many rows: the few-rows kernel, whose time grows with every 8 rows and starts again
+// every 32, while the other's is the decoding and the depth's chain. Eight 4096 x 4096 experts of 16, 32, 48, 64 rows
+// each: 88, 108, 177, 199 us by the few-rows kernel, 150, 150, 156, 156 by the other.
+constexpr int kFewRows = 32;
 constexpr size_t kTileBytes = size_t(1) << 30;  // decoded tiles of a pass
 
 struct GroupedPlan {
