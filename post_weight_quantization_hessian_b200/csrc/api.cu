@@ -640,8 +640,8 @@ int slim_token_logprobs(const void* logits, int dtype, int64_t N, int64_t V, int
   if (dtype != SLIM_X_F32 && dtype != SLIM_X_BF16) return SLIM_EINVAL;
   if (N < 0 || N > INT32_MAX || V < 1 || V > INT32_MAX || ld < V) return SLIM_EINVAL;
   if (top_k < 0 || top_k > 32 || top_k > V) return SLIM_EINVAL;
+  if (N == 0) return SLIM_OK;  // (empty outputs may have no address)
   if ((top_k > 0) != (top_logp != nullptr) || (top_k > 0) != (top_id != nullptr)) return SLIM_EINVAL;
-  if (N == 0) return SLIM_OK;
   if (!logits || !aligned_to(logits, dtype == SLIM_X_F32 ? 4 : 2) || !aligned_to(tokens, 8) || !aligned_to(logp, 4) ||
       !aligned_to(entropy, 4) || !aligned_to(top_logp, 4) || !aligned_to(top_id, 4))
     return SLIM_EINVAL;

@@ -328,3 +328,25 @@ def test_injected_failure(monkeypatch):
     with pytest.raises(slim.SlimError) as e:
         slim.slim_dequant_grouped_gemm(*dev, 64, 2, x, off)
     assert e.value.status == 7
+
+
+def test_no_rows():
+    dev = on_device(*make_layers(2, 64, 256, 64, 2, 20))
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    y = slim.slim_dequant_grouped_gemm(*dev, 64, 2, torch.zeros((0, 256), device="cuda"), off)
+    assert y.shape == (0, 64)
+    y = torch.full((70, 64), 7.0, device="cuda")                 # rows, but none of an expert
+    slim.slim_dequant_grouped_gemm(*dev, 64, 2, torch.zeros((70, 256), device="cuda"), off, y=y)
+    assert torch.equal(y, torch.full_like(y, 7.0))
+
+
+def test_offsets_that_descend_stay_inside():
+    """Offsets out of order give unspecified rows, but nothing outside y is written and the device stays usable."""
+    E, m, n, R = 9, 130, 256, 150
+    layer = make_layers(E, m, n, 64, 2, 22)
+    x, xd = make_x(R, n, "bf16", 23)
+    buf = torch.full((R + 8, m), 7.0, device="cuda")
+    off = torch.tensor([0, R, 0, R, 0, R, 0, R, 0, R], dtype=torch.int32, device="cuda")
+    slim.slim_dequant_grouped_gemm(*on_device(*layer), 64, 2, xd, off, y=buf[:R])
+    slim.slim_async_status()
+    assert torch.equal(buf[R:], torch.full_like(buf[R:], 7.0))

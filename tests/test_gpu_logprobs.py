@@ -195,3 +195,23 @@ def test_offsets_past_32_bits():
         else:
             close(a[N - 3:], b, V, what)
     assert abs(got[1][0].item() - np.log(V)) < 1e-4 and got[3][5].tolist() == [0, 1, 2, 3, 4]
+
+
+def test_empty_batch():
+    out = slim.slim_token_logprobs(torch.zeros((0, 50), device="cuda"), torch.zeros(0, dtype=torch.long, device="cuda"), top_k=3)
+    assert [tuple(t.shape) for t in out] == [(0,), (0,), (0, 3), (0, 3)]
+
+
+@pytest.mark.parametrize("V", [300, 60000])
+@pytest.mark.parametrize("left", [0, 1, 3, 31])
+def test_fewer_unmasked_logits_than_alternatives(V, left):
+    """Constrained decoding: few logits are left; the masked ones follow by index."""
+    for N in (1, 400):
+        g = torch.Generator().manual_seed(left + V)
+        l = torch.full((N, V), -float("inf"))
+        for r in range(N):
+            l[r, torch.randperm(V, generator=g)[:left]] = torch.randn(left, generator=g)
+        check(l.double().numpy()[:3], l.cuda()[:3], torch.zeros(min(N, 3), dtype=torch.long), 32)
+        one = slim.slim_token_logprobs(l[-1:].cuda(), top_k=32)
+        many = slim.slim_token_logprobs(l.cuda(), top_k=32)
+        assert torch.equal(many[3][-1:], one[3])

@@ -89,6 +89,7 @@ def test_logprobs_refusals(lib, kw, why):
 
 def test_logprobs_of_no_rows_is_ok_without_a_device(lib):
     assert lib.slim_token_logprobs(None, 0, 0, 1000, 1000, None, 0, None, None, None, None, None) == 0
+    assert lib.slim_token_logprobs(None, 0, 0, 1000, 1000, None, 5, None, None, None, None, None) == 0
 
 
 def binding_args(**kw):
