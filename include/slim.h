@@ -361,7 +361,8 @@ int slim_dequant_grouped_gemm(const uint32_t* codes, const uint8_t* bits, const 
 int slim_async_status(void* stream);
 
 /* ------------------------------------------------------------------------
- * slim_token_logprobs: what a quantized model is judged by and answers with.
+ * slim_token_logprobs: log probabilities of given tokens, entropy and top
+ * alternatives, what a quantized model's perplexity and answers come from.
  * Per row of logits, with lse = log sum_v exp(l_v) and p_v = exp(l_v - lse):
  *   logp     device N float32: l[token] - lse. May be NULL.
  *   entropy  device N float32: -sum_v p_v log p_v (natural log). May be NULL.
