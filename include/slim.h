@@ -337,9 +337,11 @@ int slim_dequant_gemv(const uint32_t* codes, const uint8_t* bits, const float* s
  *            offsets[0], behind offsets[E]) are not written.
  *   y        device R x m, row-major, float32 or bf16 (ydtype), aligned to its
  *            element.
- * 1 <= E <= 1024, E m < 2^31, 0 <= R <= 2^29, 0 <= T < 2^31; R = 0 does nothing. Sums are fp32 or better and
- * in a fixed order: the same inputs give the same y. Products take exact
- * codes; fp32 x enters as three bf16 parts (all 24 bits; |x| up to 3.38e38). The call is
+ * 1 <= E <= 1024, E m < 2^31, 0 <= R <= 2^29, 0 <= T < 2^31; R = 0 does nothing. Sums are fp32 and
+ * in a fixed order: the same inputs give the same y. Products take exact codes;
+ * fp32 x, and the scales, zeros and sums of x of experts with many rows, enter as
+ * three bf16 parts (24 bits). A y of bf16 is rounded once, at the end. The sums of x
+ * over a group and 128 times them must be finite in fp32 (|x| below 1e34 always is). The call is
  * asynchronous and can be captured into a CUDA graph; ws must then stay the
  * graph's own. A device-side failure is reported by slim_async_status.
  * Workspace: slim_dequant_grouped_gemm_workspace_bytes (it may be 0; gathered:

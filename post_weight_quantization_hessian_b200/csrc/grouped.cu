@@ -41,37 +41,42 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// A value of y: fp32, or rounded once to bf16.
+template <typename out_t>
+__device__ __forceinline__ out_t as_out(float v) {
+  if constexpr (std::is_same<out_t, float>::value)
+    return v;
+  else
+    return (out_t)pack_bf16(v, 0.f);
+}
 // v = p1 + p2 + p3, each a bf16 value (8 + 8 + 8 bits).
 __device__ __forceinline__ void split3(float v, float& p1, float& p2, float& p3) {
   p1 = __uint_as_float(pack_bf16(v, 0.f) << 16);
   p2 = __uint_as_float(pack_bf16(v - p1, 0.f) << 16);
   p3 = __uint_as_float(pack_bf16(v - p1 - p2, 0.f) << 16);
 }
-// Correction columns of one group: the products of the parts of a and b that
-// matter, side by side. Four columns (a1 b1, a1 b2, a2 b1, a2 b2) leave out about
-// 2^-17 of a b, eight (with a1 b3, a3 b1, a2 b3, a3 b2) about 2^-24.
-template <int kSlots, bool kFirst>
+// Correction columns of one group: eight products of the parts of a and b side by
+// side (a1 b1, a1 b2, a2 b1, a2 b2, a1 b3, a3 b1, a2 b3, a3 b2), all but a3 b3: about
+// 2^-32 of a b is left out. (The first four alone leave out 2^-17, which a bf16
+// result shows: 2 percent of its values rounded to the wrong side, 6 for x of mean 1.)
+constexpr int kSlots = 8;
+template <bool kFirst>
 __device__ __forceinline__ void split_slots(float v, uint32_t (&o)[kSlots / 2]) {
   float p1, p2, p3;
   split3(v, p1, p2, p3);
   if (kFirst) {
     o[0] = pack_bf16(p1, p1);
     o[1] = pack_bf16(p2, p2);
-    if constexpr (kSlots == 8) {
-      o[2] = pack_bf16(p1, p3);
-      o[3] = pack_bf16(p2, p3);
-    }
+    o[2] = pack_bf16(p1, p3);
+    o[3] = pack_bf16(p2, p3);
   } else {
     o[0] = pack_bf16(p1, p2);
     o[1] = pack_bf16(p1, p2);
-    if constexpr (kSlots == 8) {
-      o[2] = pack_bf16(p3, p1);
-      o[3] = pack_bf16(p3, p2);
-    }
+    o[2] = pack_bf16(p3, p1);
+    o[3] = pack_bf16(p3, p2);
   }
 }
 
-template <int kSlots>
 __global__ void __launch_bounds__(GP_ROWS * 32)
 gg_prep_kernel(const void* __restrict__ x, int xdtype, int64_t T, const int32_t* __restrict__ row_index, int64_t R,
                int64_t n, int group, uint16_t* __restrict__ xg, uint16_t* __restrict__ xs, int64_t xs_stride) {
@@ -111,12 +116,9 @@ gg_prep_kernel(const void* __restrict__ x, int xdtype, int64_t T, const int32_t*
     if (j >= n) continue;
     if (xs && lane % per == 0) {
       uint32_t o[kSlots / 2];
-      split_slots<kSlots, false>(s, o);
+      split_slots<false>(s, o);
       uint16_t* dst = xs + r * xs_stride + (uint32_t)j / (uint32_t)group * kSlots;
-      if constexpr (kSlots == 8)
-        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-      else
-        *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+      *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
     }
     if (xg && xdtype == 1) {
       *reinterpret_cast<uint4*>(xg + r * n + j) = make_uint4(p[0], p[1], p[2], p[3]);
@@ -147,6 +149,7 @@ gg_prep_kernel(const void* __restrict__ x, int xdtype, int64_t T, const int32_t*
 // the layer again.)
 constexpr int GT_M = 128, GT_N = 256, GT_K = 64;
 constexpr int GT_MAX_E = 1024;
+constexpr int kCorr = GT_K / kSlots;  // groups of a box of correction columns
 constexpr int GT_ABYTES = GT_M * GT_K * 2, GT_XBYTES = GT_N * GT_K * 2;
 
 struct GtParams {
@@ -193,18 +196,18 @@ __device__ __forceinline__ int gt_slots(const GtParams& p, int lane, int* s_expe
 // codes' loads where there are few blocks.
 constexpr int GD_THREADS = 256, GD_BOXES = 4;
 
-template <int B, bool kCenter>
+template <int B>
 __device__ __forceinline__ uint4 decode8(uint32_t lo, uint32_t hi) {
   uint32_t w[(B * 8 + 31) / 32], o[4];
   w[0] = lo;
   if constexpr (B > 4) w[1] = hi;
-  decode_codes<B, 8, kCenter>(w, o);
+  decode_codes<B, 8>(w, o);
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <int G, bool kCenter>
+template <int G>
 __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
-  constexpr int kSlots = kCenter ? 8 : 4, kUnits = G / 32, kCorr = GT_K / kSlots;
+  constexpr int kUnits = G / 32;
   __shared__ int s_expert[GT_MAX_E];
   __shared__ int s_count, s_before;
   __shared__ uint32_t s_width[GD_BOXES * 2];  // first word << 4 | width, of each 32-column unit
@@ -263,28 +266,21 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
           if (b > 4) hi = sh + 8 * b > 64 ? __funnelshift_r(w1, __ldg(w + 2), sh) : w1 >> sh;
         }
         switch (b) {
-          case 1: v = decode8<1, kCenter>(lo, hi); break;
-          case 2: v = decode8<2, kCenter>(lo, hi); break;
-          case 3: v = decode8<3, kCenter>(lo, hi); break;
-          case 4: v = decode8<4, kCenter>(lo, hi); break;
-          case 5: v = decode8<5, kCenter>(lo, hi); break;
-          case 6: v = decode8<6, kCenter>(lo, hi); break;
-          case 7: v = decode8<7, kCenter>(lo, hi); break;
-          case 8: v = decode8<8, kCenter>(lo, hi); break;
+          case 1: v = decode8<1>(lo, hi); break;
+          case 2: v = decode8<2>(lo, hi); break;
+          case 3: v = decode8<3>(lo, hi); break;
+          case 4: v = decode8<4>(lo, hi); break;
+          case 5: v = decode8<5>(lo, hi); break;
+          case 6: v = decode8<6>(lo, hi); break;
+          case 7: v = decode8<7>(lo, hi); break;
+          case 8: v = decode8<8>(lo, hi); break;
           default: break;
         }
       } else {
+        const int c = (kb - nbox) * kCorr + chunk, bc = c < p.k ? bits[c] : 0;
+        const float cx = bc >= 1 && bc <= 8 ? coef_x(bc, p.scale[i * p.k + c], p.zero[i * p.k + c]) : 0.f;
         uint32_t o[4];
-#pragma unroll
-        for (int z = 0; z < 8 / kSlots; ++z) {
-          const int c = (kb - nbox) * kCorr + chunk * (8 / kSlots) + z, bc = c < p.k ? bits[c] : 0;
-          const float cx =
-              bc >= 1 && bc <= 8 ? coef_x<kCenter>(bc, p.scale[i * p.k + c], p.zero[i * p.k + c]) : 0.f;
-          uint32_t part[kSlots / 2];
-          split_slots<kSlots, true>(cx, part);
-#pragma unroll
-          for (int y = 0; y < kSlots / 2; ++y) o[z * (kSlots / 2) + y] = part[y];
-        }
+        split_slots<true>(cx, o);
         v = make_uint4(o[0], o[1], o[2], o[3]);
       }
       *reinterpret_cast<uint4*>(tile + row * 128 + ((chunk ^ (row & 7)) << 4)) = v;
@@ -308,10 +304,9 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
 //                warp stores 32 consecutive outputs of a row)
 // The other term, sum over groups of coef_x xs, is a product of its own of depth
 // k: its factors are fp32, so each is cut into bf16 parts and the products of the
-// parts stand side by side as correction columns (4 a group for a bf16 y, 8 for
-// an fp32 y), which the tensor cores add up like one more group. That takes
-// 4 / group more tensor time and halves the epilogue's arithmetic, which is what
-// bounds groups of 64 and 32.
+// parts stand side by side as correction columns, 8 a group, which the tensor
+// cores add up like one more group. That takes 8 / group more tensor time and
+// halves the epilogue's arithmetic, which is what bounds groups of 64 and 32.
 // Rows of two neighbouring experts may share an x box: an accumulator column
 // depends on its own row of x alone, and only the tile's rows are stored.
 // 136 us on 4096 rows of a 4096 x 4096 layer at groups of 128 (1010 TFLOP/s), 1058 us
@@ -418,9 +413,8 @@ __device__ __forceinline__ GtTile gt_tile(const GtParams& p, int t, int slots, i
   return u;
 }
 
-template <int G, bool kCenter>
+template <int G, typename out_t>
 __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_constant__ GtMaps tm, const GtParams p) {
-  constexpr int kCorr = GT_K / (kCenter ? 8 : 4);  // groups of a correction box
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + GT_OFF_BAR);
@@ -515,7 +509,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
             s4 = sn;
             sn = load4(c + 4);
           }
-          cd = bnext >= 1 && bnext <= 8 ? coef_d<kCenter>(bnext, s4.x) : 0.f;
+          cd = bnext >= 1 && bnext <= 8 ? coef_d(bnext, s4.x) : 0.f;
           s4 = make_float4(s4.y, s4.z, s4.w, 0.f);
           if (c + 1 < p.k) bnext = bits[c + 1];
         }
@@ -544,7 +538,6 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
         dr.step(2);
       }
       if (!ok) break;
-      using out_t = typename std::conditional<kCenter, float, uint16_t>::type;
       const int cols = row_ok ? min(u.N, u.r1 - u.col0) : 0;
       out_t* yp = static_cast<out_t*>(p.y) + (int64_t)(u.col0 + half * 32) * p.m + i;
 #pragma unroll
@@ -558,10 +551,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
             gt_unpack(acc[q * 16 + v / 2], a, b);
             const float val = v & 1 ? b : a;
             if (v < left) {
-              if constexpr (kCenter)
-                *yc = val;
-              else
-                *yc = (uint16_t)pack_bf16(val, 0.f);
+              *yc = as_out<out_t>(val);
             }
             yc += p.m;
           }
@@ -778,7 +768,7 @@ __device__ __forceinline__ void gs_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
 }
 
 // kNT: tiles of 8 rows at a time; kPlanes: bf16 planes of x.
-template <int G, bool kCenter, int kNT, int kPlanes>
+template <int G, typename out_t, int kNT, int kPlanes>
 __global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
   constexpr int kUnits = G / 32, kGroups = GS_K / G, kRows = 8 * kNT;
   constexpr int kSub = G == 32 ? 32 : 64, kCodes = kSub / 4;  // columns decoded at a time, and a thread's of a row
@@ -932,7 +922,7 @@ __global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
       for (int c = 0; c < kHalf; ++c) {
         const int at = ch * kGroups + chalf + c, b = at < p.k ? s_width[at] & 15 : 0;
         s_coef[ch & 1][chalf + c][tid & (GS_M - 1)] =
-            b ? make_float2(coef_d<kCenter>(b, sreg[c]), coef_x<kCenter>(b, sreg[c], zreg[c])) : make_float2(0.f, 0.f);
+            b ? make_float2(coef_d(b, sreg[c]), coef_x(b, sreg[c], zreg[c])) : make_float2(0.f, 0.f);
       }
       if (ch + 1 < ch1) load_scales(ch + 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(GS_STAGES - 2) : "memory");
@@ -998,7 +988,7 @@ __global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
         }                                                                                                     \
       }                                                                                                       \
       _Pragma("unroll") for (int q = 0; q < kWords; ++q) v[q] = kShift ? __funnelshift_r(w[q], w[q + 1], sh) : w[q]; \
-      decode_codes<B, kCodes, kCenter>(v, A[r]);                                                              \
+      decode_codes<B, kCodes>(v, A[r]);                                                                       \
     }                                                                                                         \
   } break;
             GS_CASE(1) GS_CASE(2) GS_CASE(3) GS_CASE(4) GS_CASE(5) GS_CASE(6) GS_CASE(7) GS_CASE(8)
@@ -1093,10 +1083,7 @@ __global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
         sum += f;
       }
       const int64_t to = (int64_t)(q0 + r) * p.m + m0 + o;
-      if constexpr (kCenter)
-        static_cast<float*>(p.y)[to] = sum;
-      else
-        static_cast<uint16_t*>(p.y)[to] = (uint16_t)pack_bf16(sum, 0.f);
+      static_cast<out_t*>(p.y)[to] = as_out<out_t>(sum);
     }
     if (p.split > 1) {
       asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -1122,14 +1109,13 @@ struct GroupedPlan {
   size_t off_xg, off_tiles, bytes;
 };
 
-// For an fp32 y the correction columns are 8 a group; the plan has room for either.
 static GroupedPlan grouped_plan(int64_t E, int64_t m, int64_t n, int group, int xdtype, bool gathered, int64_t R) {
   GroupedPlan g{};
-  const int64_t k = n / group, boxes = (n + GT_K - 1) / GT_K + (k + 7) / 8;
+  const int64_t k = n / group, boxes = (n + GT_K - 1) / GT_K + (k + kCorr - 1) / kCorr;
   g.slots = std::min<int64_t>(E, R / (kFewRows + 1));
   g.mtiles = (m + GT_M - 1) / GT_M;
   g.planes = xdtype == 0 ? 3 : (gathered && g.slots ? 1 : 0);
-  g.xs_stride = k * 8;
+  g.xs_stride = k * kSlots;
   if (g.slots) {
     const size_t each = (size_t)g.slots * boxes * GT_ABYTES;  // one output tile of every slot
     g.mt = std::min<int64_t>(g.mtiles, std::max<int64_t>(1, (int64_t)(kTileBytes / each)));
@@ -1145,34 +1131,33 @@ size_t grouped_workspace_bytes(int64_t E, int64_t m, int64_t n, int group, int x
   return grouped_plan(E, m, n, group, xdtype, gathered, R).bytes;
 }
 
-template <int G, bool kCenter>
+template <int G, typename out_t>
 static cudaError_t launch_many(const GtMaps& tm, GtParams p, const GroupedPlan& g, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> attr{0};
   uint64_t bit = 0;
   if (attr_pending(attr, bit)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(gg_tc_kernel<G, kCenter>, cudaFuncAttributeMaxDynamicSharedMemorySize, GT_SMEM);
+        cudaFuncSetAttribute(gg_tc_kernel<G, out_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, GT_SMEM);
     if (e != cudaSuccess) return e;
     attr.fetch_or(bit);
   }
-  constexpr int kCorr = GT_K / (kCenter ? 8 : 4);
   const int boxes = (int)((p.n + GT_K - 1) / GT_K) + (p.k + kCorr - 1) / kCorr;
   for (int64_t mt = 0; mt < g.mtiles; mt += g.mt) {
     p.mt0 = (int)mt;
     p.mtn = (int)std::min<int64_t>(g.mt, g.mtiles - mt);
-    gd_kernel<G, kCenter><<<dim3((boxes + GD_BOXES - 1) / GD_BOXES, p.mtn, (unsigned)g.slots), GD_THREADS, 0, s>>>(p);
-    gg_tc_kernel<G, kCenter><<<num_sms, GT_THREADS, GT_SMEM, s>>>(tm, p);
+    gd_kernel<G><<<dim3((boxes + GD_BOXES - 1) / GD_BOXES, p.mtn, (unsigned)g.slots), GD_THREADS, 0, s>>>(p);
+    gg_tc_kernel<G, out_t><<<num_sms, GT_THREADS, GT_SMEM, s>>>(tm, p);
     count_launches(2);
   }
   return cudaGetLastError();
 }
 
-template <int G, bool kCenter, int kNT, int kPlanes>
+template <int G, typename out_t, int kNT, int kPlanes>
 static cudaError_t launch_few(GsParams p, int64_t slots, int avg_bits, int num_sms, cudaStream_t s) {
   static std::atomic<uint64_t> attr{0};
   uint64_t bit = 0;
   if (attr_pending(attr, bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(gs_kernel<G, kCenter, kNT, kPlanes>,
+    const cudaError_t e = cudaFuncSetAttribute(gs_kernel<G, out_t, kNT, kPlanes>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
     if (e != cudaSuccess) return e;
     attr.fetch_or(bit);
@@ -1200,18 +1185,18 @@ static cudaError_t launch_few(GsParams p, int64_t slots, int avg_bits, int num_s
   cfg.attrs = at;
   cfg.numAttrs = 1;
   count_launches(1);
-  return cudaLaunchKernelEx(&cfg, gs_kernel<G, kCenter, kNT, kPlanes>, p);
+  return cudaLaunchKernelEx(&cfg, gs_kernel<G, out_t, kNT, kPlanes>, p);
 }
 
-template <int G, bool kCenter>
+template <int G, typename out_t>
 static cudaError_t launch_few_of(const GsParams& p, int planes, int64_t slots, int64_t R, int avg_bits, int num_sms,
                                  cudaStream_t s) {
   if (planes == 3)
-    return R <= 8 ? launch_few<G, kCenter, 1, 3>(p, slots, avg_bits, num_sms, s)
-                  : launch_few<G, kCenter, 2, 3>(p, slots, avg_bits, num_sms, s);
-  if (R <= 8) return launch_few<G, kCenter, 1, 1>(p, slots, avg_bits, num_sms, s);
-  return R <= 16 ? launch_few<G, kCenter, 2, 1>(p, slots, avg_bits, num_sms, s)
-                 : launch_few<G, kCenter, 4, 1>(p, slots, avg_bits, num_sms, s);
+    return R <= 8 ? launch_few<G, out_t, 1, 3>(p, slots, avg_bits, num_sms, s)
+                  : launch_few<G, out_t, 2, 3>(p, slots, avg_bits, num_sms, s);
+  if (R <= 8) return launch_few<G, out_t, 1, 1>(p, slots, avg_bits, num_sms, s);
+  return R <= 16 ? launch_few<G, out_t, 2, 1>(p, slots, avg_bits, num_sms, s)
+                 : launch_few<G, out_t, 4, 1>(p, slots, avg_bits, num_sms, s);
 }
 
 cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const float* scale, const float* zero,
@@ -1225,10 +1210,7 @@ cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const flo
   cudaError_t e = cudaSuccess;
   if (xs || xg) {
     const dim3 blocks((unsigned)((R + GP_ROWS - 1) / GP_ROWS), (unsigned)((n + GP_COLS - 1) / GP_COLS));
-    if (ydtype == 0)
-      gg_prep_kernel<8><<<blocks, GP_ROWS * 32, 0, s>>>(x, xdtype, T, row_index, R, n, group, xg, xs, g.xs_stride);
-    else
-      gg_prep_kernel<4><<<blocks, GP_ROWS * 32, 0, s>>>(x, xdtype, T, row_index, R, n, group, xg, xs, g.xs_stride);
+    gg_prep_kernel<<<blocks, GP_ROWS * 32, 0, s>>>(x, xdtype, T, row_index, R, n, group, xg, xs, g.xs_stride);
     count_launches(1);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -1246,8 +1228,8 @@ cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const flo
   const int planes = xdtype == 0 ? 3 : 1;
   const int64_t few = std::min<int64_t>(E, R);
 #define SLIM_GS(G)                                                                  \
-  (ydtype == 0 ? launch_few_of<G, true>(f, planes, few, R, avg_bits, num_sms, s)    \
-               : launch_few_of<G, false>(f, planes, few, R, avg_bits, num_sms, s))
+  (ydtype == 0 ? launch_few_of<G, float>(f, planes, few, R, avg_bits, num_sms, s)   \
+               : launch_few_of<G, uint16_t>(f, planes, few, R, avg_bits, num_sms, s))
   e = group == 32 ? SLIM_GS(32) : (group == 64 ? SLIM_GS(64) : SLIM_GS(128));
 #undef SLIM_GS
   if (e != cudaSuccess || g.slots == 0) return e;
@@ -1257,17 +1239,16 @@ cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const flo
   p.m = m; p.n = n; p.R = R; p.rw = rw;
   p.E = (int)E; p.k = k; p.planes = planes; p.few_rows = kFewRows;
   p.max_slots = (int)g.slots;
-  const int slots = ydtype == 0 ? 8 : 4;
   GtMaps tm;
   const void* xb = xg ? static_cast<const void*>(xg) : x;
   const uint64_t rows = xg ? (uint64_t)g.planes * R : (uint64_t)T;
   const uint64_t xs_bytes = (uint64_t)g.xs_stride * 2;
   if (!make_tmap_bf16(&tm.x256, xb, (uint64_t)n, rows, GT_K, GT_N) ||
       !make_tmap_bf16(&tm.x32, xb, (uint64_t)n, rows, GT_K, 32) ||
-      !make_tmap_2byte_strided(&tm.s256, xs, (uint64_t)k * slots, (uint64_t)R, xs_bytes, GT_K, GT_N) ||
-      !make_tmap_2byte_strided(&tm.s32, xs, (uint64_t)k * slots, (uint64_t)R, xs_bytes, GT_K, 32))
+      !make_tmap_2byte_strided(&tm.s256, xs, (uint64_t)k * kSlots, (uint64_t)R, xs_bytes, GT_K, GT_N) ||
+      !make_tmap_2byte_strided(&tm.s32, xs, (uint64_t)k * kSlots, (uint64_t)R, xs_bytes, GT_K, 32))
     return cudaErrorInvalidValue;
-#define SLIM_GT(G) (ydtype == 0 ? launch_many<G, true>(tm, p, g, num_sms, s) : launch_many<G, false>(tm, p, g, num_sms, s))
+#define SLIM_GT(G) (ydtype == 0 ? launch_many<G, float>(tm, p, g, num_sms, s) : launch_many<G, uint16_t>(tm, p, g, num_sms, s))
   return group == 32 ? SLIM_GT(32) : (group == 64 ? SLIM_GT(64) : SLIM_GT(128));
 #undef SLIM_GT
 }
