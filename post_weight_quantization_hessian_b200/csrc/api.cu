@@ -85,7 +85,6 @@ thread_local std::string g_last_cuda_error;
 thread_local int g_last_detail = 0;
 constexpr double kDampAlpha = 0.01;
 constexpr size_t kStatusBytes = sizeof(DevStatus);
-constexpr int kMaxGroups = 1024;
 
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -127,7 +126,7 @@ int check_shape(int64_t m, int64_t n, int64_t N, int xdtype, int group) {
   if (group != 32 && group != 64 && group != 128) return SLIM_EINVAL;
   if (n % group != 0) return SLIM_EINVAL;
   if (n / group > kMaxGroups) return SLIM_EINVAL;
-  if (n > 65535 || m > (int64_t)1 << 30 || N > (int64_t)1 << 31) return SLIM_EINVAL;
+  if (n > kMaxColumns || m > (int64_t)1 << 30 || N > (int64_t)1 << 31) return SLIM_EINVAL;
   if (xdtype != SLIM_X_F32 && xdtype != SLIM_X_BF16) return SLIM_EINVAL;
   return SLIM_OK;
 }

@@ -39,6 +39,10 @@ struct DevStatus {
 };
 static_assert(sizeof(DevStatus) == 256, "status area is 256 bytes");
 
+// The widest layer that the entry points accept: input columns, and groups of them.
+constexpr int kMaxColumns = 65535;
+constexpr int kMaxGroups = 1024;
+
 constexpr int kStatusInvalid = 1;   // a device-side argument check failed (SLIM_EINVAL)
 constexpr int kStatusTimeout = 4;
 constexpr int kStatusNotPD = 5;

@@ -734,6 +734,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
 // 10.4 us for one row of a 4096 x 4096 layer (5.3 MB), 80 for eight rows over five
 // 11008 x 4096 experts (71 MB, 0.89 TB/s).
 constexpr int GS_THREADS = 256, GS_M = 128, GS_K = 256, GS_STAGES = 2;
+// What the tables in shared memory hold: the widest layer that the entry point accepts.
+constexpr int GS_MAX_CHUNKS = (kMaxColumns + GS_K - 1) / GS_K;
 // Bytes of a row of x: the 16-byte reads of two rows and four threads meet no bank twice.
 __host__ __device__ constexpr int gs_xstride(int group) { return GS_K * 2 + (group == 32 ? 64 : 16); }
 
@@ -775,8 +777,8 @@ __global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
   constexpr int GS_XSTRIDE = gs_xstride(G);
   extern __shared__ __align__(16) uint8_t gs_smem[];
   __shared__ int s_expert, s_found;
-  __shared__ uint32_t s_width[1024];               // first word << 4 | width of each group
-  __shared__ int2 s_words[1024 * 32 / GS_K];       // first and last word of each chunk
+  __shared__ uint32_t s_width[kMaxGroups];         // first word << 4 | width of each group
+  __shared__ int2 s_words[GS_MAX_CHUNKS];          // first and last word of each chunk
   __shared__ float2 s_coef[2][kGroups][GS_M];      // coef_d, coef_x
   __shared__ int s_row[kRows];                     // row of x, -1: zeros
   __shared__ float2 s_sum[GS_K / 32][kRows / 2];   // sums of x over 32 columns, of two rows
