@@ -348,9 +348,13 @@ class _on:
         if stream is None:
             self.raw = torch.cuda.current_stream(device).cuda_stream
         else:
-            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
-            self.guards.append(torch.cuda.stream(s))
-            self.raw = s.cuda_stream
+            self.raw = _stream(stream)
+            if not hasattr(stream, "cuda_stream"):
+                # 0 is the default stream's handle; as a handle from outside, torch takes it for "none given" and
+                # returns a stream of its own pool
+                stream = (torch.cuda.ExternalStream(self.raw, device=device) if self.raw
+                          else torch.cuda.default_stream(device))
+            self.guards.append(torch.cuda.stream(stream))
 
     def __enter__(self):
         for g in self.guards:
