@@ -359,7 +359,8 @@ int slim_dequant_grouped_gemm(const uint32_t* codes, const uint8_t* bits, const 
 /* The device-side status of the asynchronous calls made on the current device
  * since the last query: waits for `stream`, returns SLIM_OK or SLIM_ETIMEOUT
  * (a bounded wait of slim_dequant_grouped_gemm gave up; its y is unspecified)
- * and clears it. */
+ * and clears it. The status is read and cleared in one step: calls that still run on
+ * other streams report to the next query. */
 int slim_async_status(void* stream);
 
 /* ------------------------------------------------------------------------

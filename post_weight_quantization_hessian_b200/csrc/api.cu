@@ -66,7 +66,7 @@ cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const flo
 cudaError_t launch_logprobs(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const int64_t* tokens,
                             int top_k, float* logp, float* entropy, float* top_logp, int32_t* top_id, int num_sms,
                             cudaStream_t s);
-cudaError_t take_async_status(DevStatus* host, cudaStream_t s);
+cudaError_t take_async_status(int* code, int* where, uint8_t* tmp, cudaStream_t s);
 cudaError_t launch_gptq(const float* W, int64_t m, int64_t n, const double* H, double alpha, const uint8_t* bits,
                         int group, int avg_bits, double lam, int n_tau, uint32_t* codes, float* scale, float* zero,
                         uint8_t* tau_idx, double* h, double* ws, DevStatus* st, int num_sms, cudaStream_t s);
@@ -628,10 +628,15 @@ int slim_async_status(void* stream) {
   int sms = 0;
   int rc = device_sms(&sms);
   if (rc) return rc;
-  DevStatus hs;
-  SLIM_CUDA(take_async_status(&hs, static_cast<cudaStream_t>(stream)));
-  g_last_detail = hs.code ? hs.where : 0;
-  return hs.code == 0 ? SLIM_OK : hs.code == kStatusTimeout ? SLIM_ETIMEOUT : SLIM_ECUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Workspace w;
+  w.sync_on_release = false;
+  rc = w.acquire(nullptr, 0, kStatusBytes, s);
+  if (rc) return rc;
+  int code = 0, where = 0;
+  SLIM_CUDA(take_async_status(&code, &where, w.p, s));
+  g_last_detail = code ? where : 0;
+  return code == 0 ? SLIM_OK : code == kStatusTimeout ? SLIM_ETIMEOUT : SLIM_ECUDA;
 }
 
 int slim_token_logprobs(const void* logits, int dtype, int64_t N, int64_t V, int64_t ld, const int64_t* tokens,

@@ -9,6 +9,7 @@
 // and zero are applied to D and to xs = sum_j x_j in fp32: no weight is rounded.
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 #include <type_traits>
 #include "common.cuh"
 #include "decode.cuh"
@@ -16,15 +17,27 @@
 
 namespace slim {
 
-// Where the asynchronous kernels of the current device record a failure; read
-// and cleared by slim_async_status.
-__device__ DevStatus g_async_status;
+// Where the asynchronous kernels of the current device record their first failure
+// (where << 32 | code, 0: none), read and cleared by slim_async_status in one
+// exchange: a failure that another stream records meanwhile is kept for the next query.
+__device__ unsigned long long g_async_status;
 
-cudaError_t take_async_status(DevStatus* host, cudaStream_t s) {
-  static const DevStatus clear = {};
-  cudaError_t e = cudaMemcpyFromSymbolAsync(host, g_async_status, sizeof(DevStatus), 0, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_async_status, &clear, sizeof(DevStatus), 0, cudaMemcpyHostToDevice, s);
-  return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
+__device__ __forceinline__ void record_async(int code, int where) {
+  atomicCAS(&g_async_status, 0ull, (unsigned long long)(uint32_t)where << 32 | (uint32_t)code);
+}
+__global__ void take_status_kernel(unsigned long long* out) { *out = atomicExch(&g_async_status, 0ull); }
+
+// tmp: 8 bytes of device memory. Waits for the stream.
+cudaError_t take_async_status(int* code, int* where, uint8_t* tmp, cudaStream_t s) {
+  unsigned long long v = 0;
+  take_status_kernel<<<1, 1, 0, s>>>(reinterpret_cast<unsigned long long*>(tmp));
+  count_launches(1);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&v, tmp, sizeof(v), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  *code = (int)(uint32_t)v;
+  *where = (int)(uint32_t)(v >> 32);
+  return e;
 }
 
 // ---------------------------------------------------------------- preparation
@@ -151,6 +164,7 @@ constexpr int GT_M = 128, GT_N = 256, GT_K = 64;
 constexpr int GT_MAX_E = 1024;
 constexpr int kCorr = GT_K / kSlots;  // groups of a box of correction columns
 constexpr int GT_ABYTES = GT_M * GT_K * 2, GT_XBYTES = GT_N * GT_K * 2;
+constexpr int kWaitPolls = 100000;  // of a bounded wait: about 2 s
 
 struct GtParams {
   const uint32_t* codes;
@@ -162,6 +176,7 @@ struct GtParams {
   void* y;
   int64_t m, n, R, rw;
   int E, k, planes, few_rows, max_slots;
+  int acc_polls;   // limit of the epilogue's wait for an accumulator (normally kWaitPolls)
   int mt0, mtn;    // output tiles of this pass: first, count
 };
 struct GtMaps {
@@ -367,10 +382,10 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // waiting warps take no issue slots from the working ones; the limit on polls
 // (a healthy phase completes in microseconds) turns a would-be hang into a
 // recorded failure. (%globaltimer is not read here: that costs more than a phase.)
-constexpr int kWaitPolls = 100000;
-__device__ __forceinline__ bool gt_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int where) {
+__device__ __forceinline__ bool gt_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int where,
+                                        int polls = kWaitPolls) {
 #pragma unroll 1
-  for (int it = 0; it < kWaitPolls; ++it) {
+  for (int it = 0; it < polls; ++it) {
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
@@ -425,6 +440,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   int* s_slots = reinterpret_cast<int*>(tslot + 2);
+  volatile uint32_t* s_issued = tslot + 4;   // stages that the copies filled, and that the gate arrived on,
+  volatile uint32_t* s_arrived = tslot + 5;  // in all, when their loops ended
   int* s_first = reinterpret_cast<int*>(smem + GT_OFF_E);
   int* s_expert = s_first + GT_MAX_E + 1;
 
@@ -514,7 +531,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
           if (c + 1 < p.k) bnext = bits[c + 1];
         }
         const uint64_t cd2 = gt_pack(cd, cd);
-        if (!gt_wait(smem_u32(dfull) + 8 * dr.slot, dr.phase, abort_flag, 11)) {
+        if (!gt_wait(smem_u32(dfull) + 8 * dr.slot, dr.phase, abort_flag, 11, p.acc_polls)) {
           ok = false;
           break;
         }
@@ -594,12 +611,11 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
           }
         }
       }
-      // let every issued copy land before the CTA can exit, also after an abort
-      for (uint32_t j = issued > stages ? issued - stages : 0; !ok && j < issued; ++j)
-        mbar_drain(&full[j % stages], (j / stages) & 1);
+      *s_issued = issued;
     } else if (warp == 10 && lane == 0) {
       // ---------------------------------------------------------- gate
       GtRing r, dr;
+      uint32_t arrived = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
         for (int kb = 0; kb < nbox + ncor && ok; ++kb) {
@@ -615,11 +631,15 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
                 ok = gt_wait(smem_u32(dempty) + 8 * dr.slot, dr.phase ^ 1, abort_flag, 32);
                 dr.step(2);
               }
-            if (ok) mbar_arrive(&full[r.slot]);
+            if (ok) {
+              mbar_arrive(&full[r.slot]);
+              ++arrived;
+            }
             r.step(stages);
           }
         }
       }
+      *s_arrived = arrived;
     } else if (warp == 9) {
       // ---------------------------------------------------------- matrix products
       // The whole warp runs the loop (uniform control and registers); one elected
@@ -706,7 +726,17 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
     __syncwarp();
   }
   __syncthreads();
-  if (tid == 0 && *abort_flag) record_failure(&g_async_status, kStatusTimeout, *abort_flag);
+  if (*abort_flag && tid == 256) {
+    record_async(kStatusTimeout, *abort_flag);
+    // Every issued copy lands before the CTA can exit, whichever role gave up. A stage's phase ends with the
+    // gate's arrival too: those that it left out are made up first. One limit for all of them.
+    const uint32_t issued = *s_issued;
+    for (uint32_t j = *s_arrived; j < issued; ++j) mbar_arrive(&full[j % stages]);
+    const uint64_t t0 = global_ns();
+    for (uint32_t j = issued > stages ? issued - stages : 0; j < issued; ++j)
+      while (!mbar_try_wait(&full[j % stages], (j / stages) & 1) && global_ns() - t0 < kWaitLimitNs) {
+      }
+  }
   if (warp == 11) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
@@ -1201,6 +1231,14 @@ static cudaError_t launch_few_of(const GsParams& p, int planes, int64_t slots, i
                  : launch_few<G, out_t, 4, 1>(p, slots, avg_bits, num_sms, s);
 }
 
+// The limit of the epilogue's wait, in polls. Tests shorten it by SLIM_TEST_GROUPED_POLLS (0: runs out at once) to
+// check that a wait that runs out is reported and leaves the device usable. Nothing else reads it.
+static int acc_polls() {
+  const char* t = std::getenv("SLIM_TEST_GROUPED_POLLS");
+  const int v = t ? std::atoi(t) : kWaitPolls;
+  return v >= 0 && v < kWaitPolls ? v : kWaitPolls;
+}
+
 cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const float* scale, const float* zero,
                            int64_t E, int64_t m, int64_t n, int group, int avg_bits, const void* x, int xdtype,
                            int64_t T, const int32_t* row_index, const int32_t* offsets, int64_t R, void* y,
@@ -1241,6 +1279,7 @@ cudaError_t launch_grouped(const uint32_t* codes, const uint8_t* bits, const flo
   p.m = m; p.n = n; p.R = R; p.rw = rw;
   p.E = (int)E; p.k = k; p.planes = planes; p.few_rows = kFewRows;
   p.max_slots = (int)g.slots;
+  p.acc_polls = acc_polls();
   GtMaps tm;
   const void* xb = xg ? static_cast<const void*>(xg) : x;
   const uint64_t rows = xg ? (uint64_t)g.planes * R : (uint64_t)T;
