@@ -345,8 +345,11 @@ int slim_dequant_gemv(const uint32_t* codes, const uint8_t* bits, const float* s
  * asynchronous and can be captured into a CUDA graph; ws must then stay the
  * graph's own. A device-side failure is reported by slim_async_status.
  * Workspace: slim_dequant_grouped_gemm_workspace_bytes (it may be 0; gathered:
- * whether row_index is given); ws NULL
- * takes it from the library's pool and returns it in stream order.
+ * whether row_index is given): 6 R n bytes for fp32 x; where an expert can have more
+ * than 32 rows (R > 32) also 16 R k, 2 R n for gathered bf16 x, and for the decoded
+ * weights 2 m (n + 8 k) for each of min(E, R / 33) experts (m rounded up to 128, n and
+ * 8 k to 64), 1 GiB of these at most.
+ * ws NULL takes it from the library's pool and returns it in stream order.
  */
 size_t slim_dequant_grouped_gemm_workspace_bytes(int64_t E, int64_t m, int64_t n, int group, int avg_bits,
                                                  int xdtype, int gathered, int64_t R);

@@ -153,8 +153,9 @@ gg_prep_kernel(const void* __restrict__ x, int xdtype, int64_t T, const int32_t*
 // ---------------------------------------------------------------- many rows
 // Experts with more than kFewRows rows: their codes are decoded once into bf16
 // tiles in the workspace (gd_kernel), and a tensor-core kernel (gg_tc_kernel)
-// multiplies the tiles with x, in passes over the outputs that bound the
-// workspace. (Passes whose tiles stay in L2, 64 MB, cost more in their last waves
+// multiplies the tiles with x, in passes over the outputs, and where one tile of
+// outputs of every expert is too much over the experts, that bound the
+// workspace (kTileBytes). (Passes whose tiles stay in L2, 64 MB, cost more in their last waves
 // than they saved: 1690 us against 1256 on 8192 rows over eight 11008 x 4096 experts.)
 // (A kernel that decoded each tile inside the product loop was built first: 265 us
 // on 4096 rows of a 4096 x 4096 layer, bound by the decoding warps and the
@@ -172,12 +173,13 @@ struct GtParams {
   const float* scale;
   const float* zero;
   const int32_t* offsets;
-  uint8_t* tiles;  // [slot][output tile of the pass][box] of 16 KB
+  uint8_t* tiles;  // [slot of the pass][output tile of the pass][box] of 16 KB
   void* y;
   int64_t m, n, R, rw;
   int E, k, planes, few_rows, max_slots;
   int acc_polls;   // limit of the epilogue's wait for an accumulator (normally kWaitPolls)
   int mt0, mtn;    // output tiles of this pass: first, count
+  int slot0, slots;  // its slots: first, count at most
 };
 struct GtMaps {
   CUtensorMap x256, x32, s256, s32;
@@ -186,7 +188,8 @@ struct GtMaps {
 __device__ __forceinline__ int gt_clamp(int v, int64_t R) { return max(0, min(v, (int)R)); }
 
 // The slots of the experts with more than few_rows rows, in order: s_expert[slot].
-// At most max_slots of them, which offsets that do not descend never exceed. One warp.
+// At most max_slots of them, which offsets that do not descend never exceed; returns
+// how many the pass takes, from slot0 on. One warp.
 __device__ __forceinline__ int gt_slots(const GtParams& p, int lane, int* s_expert) {
   int run = 0;
   for (int e0 = 0; e0 < p.E; e0 += 32) {
@@ -197,7 +200,7 @@ __device__ __forceinline__ int gt_slots(const GtParams& p, int lane, int* s_expe
     if (many) s_expert[run + __popc(mask & ((1u << lane) - 1))] = e;
     run += __popc(mask);
   }
-  return min(run, p.max_slots);
+  return max(0, min(min(run, p.max_slots) - p.slot0, p.slots));
 }
 
 // ---------------------------------------------------------------- decoding
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
   }
   __syncthreads();
   if (slot >= s_count) return;
-  const int e = s_expert[slot], nbox = (int)((p.n + GT_K - 1) / GT_K), ncor = (p.k + kCorr - 1) / kCorr;
+  const int e = s_expert[p.slot0 + slot], nbox = (int)((p.n + GT_K - 1) / GT_K), ncor = (p.k + kCorr - 1) / kCorr;
   const int kb0 = blockIdx.x * GD_BOXES, kb1 = min(kb0 + GD_BOXES, nbox + ncor);
   const uint8_t* bits = p.bits + (int64_t)e * p.k;
   const int64_t m0 = (int64_t)(p.mt0 + blockIdx.y) * GT_M;
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
         const int q = q0 + lane;
         int v = 0;
         if (q < slots) {
-          const int e = s_expert[q];
+          const int e = s_expert[p.slot0 + q];
           v = gt_row_tiles(gt_clamp(p.offsets[e], p.R), gt_clamp(p.offsets[e + 1], p.R), most, width) * p.mtn;
         }
         int incl = v;
@@ -490,6 +493,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
   }
   __syncthreads();
   tc_fence_after();
+  s_expert += p.slot0;
   const uint32_t tbase = *tslot;
   const int slots = s_slots[0], most = s_slots[1], tiles = s_first[slots];
   const uint32_t stages = most == 256 ? 4 : (most == 128 ? 6 : 8), stage = GT_ABYTES + most * 128;
@@ -1136,7 +1140,7 @@ constexpr size_t kTileBytes = size_t(1) << 30;  // decoded tiles of a pass
 struct GroupedPlan {
   int planes;          // bf16 planes copied in grouped order (0: x is read as it is)
   int64_t xs_stride;   // correction columns of a row
-  int64_t slots;       // experts that can have many rows
+  int64_t slots, st;   // experts that can have many rows, in all and in a pass
   int64_t mtiles, mt;  // output tiles in all and of a pass
   size_t off_xg, off_tiles, bytes;
 };
@@ -1149,10 +1153,12 @@ static GroupedPlan grouped_plan(int64_t E, int64_t m, int64_t n, int group, int 
   g.planes = xdtype == 0 ? 3 : (gathered && g.slots ? 1 : 0);
   g.xs_stride = k * kSlots;
   if (g.slots) {
-    const size_t each = (size_t)g.slots * boxes * GT_ABYTES;  // one output tile of every slot
-    g.mt = std::min<int64_t>(g.mtiles, std::max<int64_t>(1, (int64_t)(kTileBytes / each)));
+    const size_t each = (size_t)boxes * GT_ABYTES;  // one output tile of a slot: 18 MB at most
+    const int64_t fit = (int64_t)(kTileBytes / each);
+    g.st = std::min(g.slots, fit);
+    g.mt = std::min(g.mtiles, fit / g.st);
     g.off_xg = ((size_t)R * g.xs_stride * 2 + 255) & ~size_t(255);
-    g.bytes = each * g.mt;
+    g.bytes = each * g.st * g.mt;
   }
   g.off_tiles = g.off_xg + (((size_t)g.planes * R * n * 2 + 255) & ~size_t(255));
   g.bytes += g.off_tiles;
@@ -1174,12 +1180,16 @@ static cudaError_t launch_many(const GtMaps& tm, GtParams p, const GroupedPlan& 
     attr.fetch_or(bit);
   }
   const int boxes = (int)((p.n + GT_K - 1) / GT_K) + (p.k + kCorr - 1) / kCorr;
-  for (int64_t mt = 0; mt < g.mtiles; mt += g.mt) {
-    p.mt0 = (int)mt;
-    p.mtn = (int)std::min<int64_t>(g.mt, g.mtiles - mt);
-    gd_kernel<G><<<dim3((boxes + GD_BOXES - 1) / GD_BOXES, p.mtn, (unsigned)g.slots), GD_THREADS, 0, s>>>(p);
-    gg_tc_kernel<G, out_t><<<num_sms, GT_THREADS, GT_SMEM, s>>>(tm, p);
-    count_launches(2);
+  for (int64_t st = 0; st < g.slots; st += g.st) {
+    p.slot0 = (int)st;
+    p.slots = (int)std::min(g.st, g.slots - st);
+    for (int64_t mt = 0; mt < g.mtiles; mt += g.mt) {
+      p.mt0 = (int)mt;
+      p.mtn = (int)std::min<int64_t>(g.mt, g.mtiles - mt);
+      gd_kernel<G><<<dim3((boxes + GD_BOXES - 1) / GD_BOXES, p.mtn, (unsigned)p.slots), GD_THREADS, 0, s>>>(p);
+      gg_tc_kernel<G, out_t><<<num_sms, GT_THREADS, GT_SMEM, s>>>(tm, p);
+      count_launches(2);
+    }
   }
   return cudaGetLastError();
 }

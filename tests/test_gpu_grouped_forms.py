@@ -89,3 +89,13 @@ def test_several_passes_over_the_outputs(xdt, ydt, counts):
     edge = a_pass * 128
     cols = torch.cat([torch.arange(a, b) for a, b in ((0, 130), (edge - 130, edge + 130), (m - 130, m))]).cuda()
     run(counts, m, n, group, 2, xdt, ydt, cols=cols)
+
+
+def test_passes_over_the_experts():
+    """One output tile of each of 60 experts of 1023 + 128 boxes is past the tile budget: the experts go in two passes."""
+    n, group = 65472, 64
+    counts = [33 + e % 3 for e in range(60)]
+    assert output_tiles_of_a_pass(counts, n, group) == 0
+    assert TILE_BYTES // ((1023 + 128) * 16384) == 56
+    cols = torch.cat([torch.arange(0, 20), torch.arange(120, 140)]).cuda()
+    run(counts, 140, n, group, 2, "bf16", "bf16", cols=cols)
