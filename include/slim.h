@@ -330,7 +330,8 @@ int slim_dequant_gemv(const uint32_t* codes, const uint8_t* bits, const float* s
  *            row of y NaN or infinite, and no other row.
  *   row_index  device R int32, or NULL. Grouped row r reads row row_index[r]
  *            of x (row r when NULL; then T >= R). The same row of x may be read
- *            by many grouped rows; an index outside [0, T) reads as zeros.
+ *            by many grouped rows; an index outside [0, T) reads as zeros
+ *            (every index when T = 0; x may then be NULL).
  *   offsets  device E + 1 int32, non-decreasing: expert e's grouped rows are
  *            offsets[e] <= r < offsets[e + 1] (none when equal). Values are
  *            clamped to [0, R]; rows of y that belong to no expert (before

@@ -606,7 +606,7 @@ int slim_dequant_grouped_gemm(const uint32_t* codes, const uint8_t* bits, const 
   if (T < 0 || T > INT32_MAX || (!row_index && T < R)) return SLIM_EINVAL;
   if (ydtype != SLIM_X_F32 && ydtype != SLIM_X_BF16) return SLIM_EINVAL;
   if (R == 0) return SLIM_OK;
-  if (!codes || !bits || !scale || !zero || !x || !offsets || !y || !aligned16(codes) || !aligned16(x) ||
+  if (!codes || !bits || !scale || !zero || (!x && T) || !offsets || !y || !aligned16(codes) || !aligned16(x) ||
       !aligned_to(y, ydtype == SLIM_X_F32 ? 4 : 2) || !aligned_to(scale, 4) || !aligned_to(zero, 4) ||
       !aligned_to(offsets, 4) || !aligned_to(row_index, 4))
     return SLIM_EINVAL;
@@ -619,6 +619,7 @@ int slim_dequant_grouped_gemm(const uint32_t* codes, const uint8_t* bits, const 
   w.sync_on_release = false;
   rc = w.acquire(ws, ws_bytes, grouped_workspace_bytes(E, m, n, group, xdtype, row_index != nullptr, R), s);
   if (rc) return rc;
+  if (T == 0) x = codes;  // no row is read: any address will do where a copy of 0 bytes names one
   SLIM_CUDA(launch_grouped(codes, bits, scale, zero, E, m, n, group, avg_bits, x, xdtype, T, row_index, offsets, R, y,
                            ydtype, w.p, sms, s));
   return SLIM_OK;
