@@ -49,11 +49,6 @@ cudaError_t take_async_status(int* code, int* where, uint8_t* tmp, cudaStream_t 
 // written if copied).
 constexpr int GP_ROWS = 8, GP_COLS = 512;
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // A value of y: fp32, or rounded once to bf16.
 template <typename out_t>
 __device__ __forceinline__ out_t as_out(float v) {
@@ -215,11 +210,11 @@ __device__ __forceinline__ int gt_slots(const GtParams& p, int lane, int* s_expe
 constexpr int GD_THREADS = 256, GD_BOXES = 4;
 
 template <int B>
-__device__ __forceinline__ uint4 decode8(uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ uint4 decode8(uint32_t lo, uint32_t hi, uint32_t shift) {
   uint32_t w[(B * 8 + 31) / 32], o[4];
   w[0] = lo;
   if constexpr (B > 4) w[1] = hi;
-  decode_codes<B, 8>(w, o);
+  decode_codes<B, 8>(w, shift, o);
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -229,6 +224,8 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
   __shared__ int s_expert[GT_MAX_E];
   __shared__ int s_count, s_before;
   __shared__ uint32_t s_width[GD_BOXES * 2];  // first word << 4 | width, of each 32-column unit
+  constexpr int kGroups = GD_BOXES * 2 / kUnits;
+  __shared__ uint32_t s_shift[kGroups][GT_M];  // what is added to the codes
   const int tid = threadIdx.x, lane = tid & 31, slot = blockIdx.z;
   if (tid == 0) s_before = 0;
   if (tid < 32) {
@@ -242,9 +239,16 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
   const uint8_t* bits = p.bits + (int64_t)e * p.k;
   const int64_t m0 = (int64_t)(p.mt0 + blockIdx.y) * GT_M;
   uint8_t* out = p.tiles + ((int64_t)slot * p.mtn + blockIdx.y) * (nbox + ncor) * GT_ABYTES;
-  // widths before the block's boxes, then the block's own
+  // widths before the block's boxes, then the block's own; its zeros are on the way meanwhile
   int before = 0;
   const int c0 = kb0 * 2 / kUnits;
+  constexpr int kZeros = kGroups * GT_M / GD_THREADS;
+  float zeros[kZeros];
+#pragma unroll
+  for (int z = 0; z < kZeros; ++z) {
+    const int v = z * GD_THREADS + tid, c = min(c0 + v % kGroups, p.k - 1);
+    zeros[z] = __ldg(p.zero + ((int64_t)e * p.m + min(m0 + v / kGroups, p.m - 1)) * p.k + c);
+  }
   for (int c = tid; c < min(c0, p.k); c += GD_THREADS) before += bits[c] <= 8 ? bits[c] : 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -265,11 +269,18 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
     if (lane < GD_BOXES * 2) s_width[lane] = first + b > p.rw ? 0u : (uint32_t)first << 4 | (uint32_t)b;
   }
   __syncthreads();
+#pragma unroll
+  for (int z = 0; z < kZeros; ++z) {
+    const int v = z * GD_THREADS + tid, c = v % kGroups;
+    s_shift[c][v / kGroups] = code_shift(s_width[c * kUnits] & 15, zeros[z]);
+  }
+  __syncthreads();
   const int chunk = tid & 7, h = chunk >> 2;
   for (int kb = kb0; kb < kb1; ++kb) {
     const bool cor = kb >= nbox;
     uint8_t* tile = out + (int64_t)kb * GT_ABYTES;
     const uint32_t en = s_width[(kb - kb0) * 2 + h], b = en & 15, first = en >> 4;
+    const int group = ((kb - kb0) * 2 + h) / kUnits;  // of the block's
 #pragma unroll 4
     for (int row = tid >> 3; row < GT_M; row += GD_THREADS / 8) {
       const int64_t i = (int64_t)e * p.m + min(m0 + row, p.m - 1);
@@ -277,6 +288,7 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
       if (!cor) {
         const uint32_t bit = (chunk & 3) * 8 * b, sh = bit & 31;
         const uint32_t* w = p.codes + i * p.rw + first + (bit >> 5);
+        const uint32_t shift = s_shift[group][row];
         uint32_t lo = 0, hi = 0;
         if (b) {  // 8 b bits from bit `sh` on: never past the unit's b words
           const uint32_t w0 = __ldg(w), w1 = sh + 8 * b > 32 ? __ldg(w + 1) : 0u;
@@ -284,19 +296,23 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
           if (b > 4) hi = sh + 8 * b > 64 ? __funnelshift_r(w1, __ldg(w + 2), sh) : w1 >> sh;
         }
         switch (b) {
-          case 1: v = decode8<1>(lo, hi); break;
-          case 2: v = decode8<2>(lo, hi); break;
-          case 3: v = decode8<3>(lo, hi); break;
-          case 4: v = decode8<4>(lo, hi); break;
-          case 5: v = decode8<5>(lo, hi); break;
-          case 6: v = decode8<6>(lo, hi); break;
-          case 7: v = decode8<7>(lo, hi); break;
-          case 8: v = decode8<8>(lo, hi); break;
+          case 1: v = decode8<1>(lo, hi, shift); break;
+          case 2: v = decode8<2>(lo, hi, shift); break;
+          case 3: v = decode8<3>(lo, hi, shift); break;
+          case 4: v = decode8<4>(lo, hi, shift); break;
+          case 5: v = decode8<5>(lo, hi, shift); break;
+          case 6: v = decode8<6>(lo, hi, shift); break;
+          case 7: v = decode8<7>(lo, hi, shift); break;
+          case 8: v = decode8<8>(lo, hi, shift); break;
           default: break;
         }
       } else {
         const int c = (kb - nbox) * kCorr + chunk, bc = c < p.k ? bits[c] : 0;
-        const float cx = bc >= 1 && bc <= 8 ? coef_x(bc, p.scale[i * p.k + c], p.zero[i * p.k + c]) : 0.f;
+        float cx = 0.f;
+        if (bc >= 1 && bc <= 8) {
+          const float z = p.zero[i * p.k + c];
+          cx = coef_x(bc, p.scale[i * p.k + c], z, code_shift(bc, z));
+        }
         uint32_t o[4];
         split_slots<true>(cx, o);
         v = make_uint4(o[0], o[1], o[2], o[3]);
@@ -769,6 +785,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
 // 11008 x 4096 experts (71 MB, 0.89 TB/s).
 constexpr int GS_THREADS = 256, GS_M = 128, GS_K = 256, GS_STAGES = 2;
 // What the tables in shared memory hold: the widest layer that the entry point accepts.
+constexpr int GS_SMEM = 160 * 1024;  // beside 32 KB of tables; groups of 32, 7 bits, 16 rows in three planes take 130
 constexpr int GS_MAX_CHUNKS = (kMaxColumns + GS_K - 1) / GS_K;
 // Bytes of a row of x: the 16-byte reads of two rows and four threads meet no bank twice.
 __host__ __device__ constexpr int gs_xstride(int group) { return GS_K * 2 + (group == 32 ? 64 : 16); }
@@ -813,7 +830,9 @@ __global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
   __shared__ int s_expert, s_found;
   __shared__ uint32_t s_width[kMaxGroups];         // first word << 4 | width of each group
   __shared__ int2 s_words[GS_MAX_CHUNKS];          // first and last word of each chunk
-  __shared__ float2 s_coef[2][kGroups][GS_M];      // coef_d, coef_x
+  // coef_d and coef_x, and what is added to the codes; a thread's four outputs side by side
+  __shared__ __align__(16) float2 s_coef[2][kGroups][GS_M];
+  __shared__ __align__(16) uint32_t s_shift[2][kGroups][GS_M];
   __shared__ int s_row[kRows];                     // row of x, -1: zeros
   __shared__ float2 s_sum[GS_K / 32][kRows / 2];   // sums of x over 32 columns, of two rows
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
@@ -876,6 +895,7 @@ __global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
   const int64_t srow = (base + m0 + min(tid & (GS_M - 1), mrows - 1)) * p.k;
   constexpr int kHalf = kGroups / 2;
   const int chalf = (tid / GS_M) * kHalf;
+  const int sat = (tid & (GS_M - 32)) + (tid & 7) * 4 + ((tid & 31) >> 3);  // where its output stands in the tables
 
   for (int q0 = r0; q0 < r1; q0 += kRows) {
     const int rows = min(kRows, r1 - q0), nt = (rows + 7) / 8;
@@ -957,8 +977,10 @@ __global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
 #pragma unroll
       for (int c = 0; c < kHalf; ++c) {
         const int at = ch * kGroups + chalf + c, b = at < p.k ? s_width[at] & 15 : 0;
-        s_coef[ch & 1][chalf + c][tid & (GS_M - 1)] =
-            b ? make_float2(coef_d(b, sreg[c]), coef_x(b, sreg[c], zreg[c])) : make_float2(0.f, 0.f);
+        const uint32_t shift = code_shift(b, zreg[c]);
+        s_shift[ch & 1][chalf + c][sat] = shift;
+        s_coef[ch & 1][chalf + c][sat] =
+            b ? make_float2(coef_d(b, sreg[c]), coef_x(b, sreg[c], zreg[c], shift)) : make_float2(0.f, 0.f);
       }
       if (ch + 1 < ch1) load_scales(ch + 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(GS_STAGES - 2) : "memory");
@@ -1000,6 +1022,7 @@ __global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
         for (int u = 0; u < G / kSub; ++u) {
           // the thread's kCodes codes of four rows: kCodes b bits from bit `bit` of the staged row on
           const uint32_t bit = (wrel + u * (kSub / 32) * b) * 32 + t4 * kCodes * b;
+          const uint4 shifts = *reinterpret_cast<const uint4*>(&s_shift[ch & 1][c][out0 + g * 4]);
           uint32_t A[4][kCodes / 2];
           switch (b) {
 #define GS_CASE(B)                                                                                            \
@@ -1024,7 +1047,7 @@ __global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
         }                                                                                                     \
       }                                                                                                       \
       _Pragma("unroll") for (int q = 0; q < kWords; ++q) v[q] = kShift ? __funnelshift_r(w[q], w[q + 1], sh) : w[q]; \
-      decode_codes<B, kCodes>(v, A[r]);                                                                       \
+      decode_codes<B, kCodes>(v, r == 0 ? shifts.x : r == 1 ? shifts.y : r == 2 ? shifts.z : shifts.w, A[r]); \
     }                                                                                                         \
   } break;
             GS_CASE(1) GS_CASE(2) GS_CASE(3) GS_CASE(4) GS_CASE(5) GS_CASE(6) GS_CASE(7) GS_CASE(8)
@@ -1053,9 +1076,9 @@ __global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
                 }
               }
         }
-        float2 co[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) co[r] = s_coef[ch & 1][c][out0 + g + 8 * r];
+        const float4* cp = reinterpret_cast<const float4*>(&s_coef[ch & 1][c][out0 + g * 4]);
+        const float4 c01 = cp[0], c23 = cp[1];
+        const float2 co[4] = {{c01.x, c01.y}, {c01.z, c01.w}, {c23.x, c23.y}, {c23.z, c23.w}};
 #pragma unroll
         for (int q = 0; q < kNT; ++q)
           if (q < nt) {
@@ -1200,7 +1223,7 @@ static cudaError_t launch_few(GsParams p, int64_t slots, int avg_bits, int num_s
   uint64_t bit = 0;
   if (attr_pending(attr, bit)) {
     const cudaError_t e = cudaFuncSetAttribute(gs_kernel<G, out_t, kNT, kPlanes>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, GS_SMEM);
     if (e != cudaSuccess) return e;
     attr.fetch_or(bit);
   }

@@ -1,10 +1,11 @@
 """slim_dequant_grouped_gemm on inputs of one sign or with a mean (activations behind a ReLU, for example).
 
-Tolerance. With x of magnitude a, u = s 2^b the groups' span and v = (q - mid) 2^-b, a result is
-sum_c u (sum_j x_j v_j + (mid - z) 2^-b sum_j x_j). Codes are uniform and zeros within 0.1 of the range of mid, so
+Tolerance. With x of magnitude a, u = s 2^b the groups' span and v = (q - c) 2^-b, c any number within 0.1 of the range of
+the zero z, a result is sum_c u (sum_j x_j v_j + (c - z) 2^-b sum_j x_j). Codes are uniform and zeros within 0.1 of the
+range of its middle, so
   y's rms       Y = a u sqrt(n / 12 + k (0.058 g)^2),
-  the groups' sums of x v are a u sqrt(g / 12) each, Y at most when k of them are joined at random,
-  the running sum of the zeros' terms is a u 0.058 g sqrt(k), Y at most.
+  the groups' sums of x v are at most that of a group's share of y, Y when k of them are joined at random,
+  the running sum of the zeros' terms is at most a u 0.058 g sqrt(k), Y at most.
 The tensor core may truncate every step at 2^-23 of the running sum; a group takes g / 16 steps (three times as many
 for fp32 x), the zeros' terms, eight columns a group, k / 2, and the groups join in k fp32 additions of 2^-24. With
 sums up to 3 times their rms an output is off by at most
