@@ -364,7 +364,8 @@ int slim_dequant_grouped_gemm(const uint32_t* codes, const uint8_t* bits, const 
  * since the last query: waits for `stream`, returns SLIM_OK or SLIM_ETIMEOUT
  * (a bounded wait of slim_dequant_grouped_gemm gave up; its y is unspecified)
  * and clears it. The status is read and cleared in one step: calls that still run on
- * other streams report to the next query. */
+ * other streams report to the next query. A stream that is being captured has
+ * nothing to wait for yet: SLIM_EINVAL, and the capture goes on. */
 int slim_async_status(void* stream);
 
 /* ------------------------------------------------------------------------

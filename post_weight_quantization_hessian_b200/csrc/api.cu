@@ -630,6 +630,9 @@ int slim_async_status(void* stream) {
   int rc = device_sms(&sms);
   if (rc) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  SLIM_CUDA(cudaStreamIsCapturing(s, &capturing));
+  if (capturing != cudaStreamCaptureStatusNone) return SLIM_EINVAL;
   Workspace w;
   w.sync_on_release = false;
   rc = w.acquire(nullptr, 0, kStatusBytes, s);

@@ -81,3 +81,18 @@ def test_captured_call_reports(monkeypatch):
         with pytest.raises(slim.SlimError):
             slim.slim_async_status()
     slim.slim_async_status()
+
+
+def test_refused_on_a_stream_that_is_being_captured():
+    call = setup(200)
+    want = call()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        got = call()
+        with pytest.raises(slim.SlimError) as e:
+            slim.slim_async_status()
+    assert e.value.status == 1
+    g.replay()
+    slim.slim_async_status()
+    assert torch.equal(got, want)
