@@ -150,12 +150,13 @@ gg_prep_kernel(const void* __restrict__ x, int xdtype, int64_t T, const int32_t*
 // tiles in the workspace (gd_kernel), and a tensor-core kernel (gg_tc_kernel)
 // multiplies the tiles with x, in passes over the outputs, and where one tile of
 // outputs of every expert is too much over the experts, that bound the
-// workspace (kTileBytes). (Passes whose tiles stay in L2, 64 MB, cost more in their last waves
-// than they saved: 1690 us against 1256 on 8192 rows over eight 11008 x 4096 experts.)
+// workspace (kTileBytes). (Passes whose tiles stay in L2, 64 MB, cost more in their
+// last waves than they saved: a third more time on 8192 rows over eight 11008 x 4096
+// experts.)
 // (A kernel that decoded each tile inside the product loop was built first: 265 us
-// on 4096 rows of a 4096 x 4096 layer, bound by the decoding warps and the
-// barriers between the roles, a wait of 150 cycles each; every 256 rows decoded
-// the layer again.)
+// on 4096 rows of a 4096 x 4096 layer where the two take 151, bound by the decoding
+// warps and the barriers between the roles, a wait of 150 cycles each; every 256
+// rows decoded the layer again.)
 constexpr int GT_M = 128, GT_N = 256, GT_K = 64;
 constexpr int GT_MAX_E = 1024;
 constexpr int kCorr = GT_K / kSlots;  // groups of a box of correction columns
@@ -204,9 +205,9 @@ __device__ __forceinline__ int gt_slots(const GtParams& p, int lane, int* s_expe
 // bf16 values where the product's shared-memory layout wants them (K-major, 128-
 // byte swizzle), so that a warp writes 512 consecutive bytes and the product
 // loads a whole tile with one bulk copy. Behind the boxes of codes come those of
-// the correction columns. Bound by the bytes written (2 a weight: 14 us for a 4096 x
-// 4096 layer, 171 us for eight of 11008 x 4096, 4.3 TB/s) and by the latency of the
-// codes' loads where there are few blocks.
+// the correction columns. Bound by the bytes written (2 a weight: 13 us for a 4096 x
+// 4096 layer, 196 us for eight of 11008 x 4096, 4.1 TB/s) and by the latency of the
+// loads of codes and zeros where there are few blocks.
 constexpr int GD_THREADS = 256, GD_BOXES = 4;
 
 template <int B>
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
   for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   if (lane == 0) atomicAdd(&s_before, before);  // (integers: the order does not matter)
   __syncthreads();
-  if (tid < 32) {  // lane = unit of the block (the first may lie inside a group)
+  if (tid < 32) {  // lane = unit of the block, which starts with a group (a multiple of 256 columns)
     const int unit = kb0 * 2 + lane, c = unit / kUnits;
     int b = c < p.k && lane < GD_BOXES * 2 ? bits[c] : 0;
     if (b > 8) b = 0;
@@ -343,8 +344,8 @@ __global__ void __launch_bounds__(GD_THREADS) gd_kernel(const GtParams p) {
 // halves the epilogue's arithmetic, which is what bounds groups of 64 and 32.
 // Rows of two neighbouring experts may share an x box: an accumulator column
 // depends on its own row of x alone, and only the tile's rows are stored.
-// 136 us on 4096 rows of a 4096 x 4096 layer at groups of 128 (1010 TFLOP/s), 1058 us
-// on 8192 rows over eight 11008 x 4096 experts at groups of 64 (698): what bounds it is
+// 138 us on 4096 rows of a 4096 x 4096 layer at groups of 128 (996 TFLOP/s), 1100 us
+// on 8192 rows over eight 11008 x 4096 experts at groups of 64 (672): what bounds it is
 // the chain of an accumulator's hand-over (commit, wait, loads and additions,
 // wait), about 1000 cycles a group besides the 256 to 1024 of its products.
 constexpr int GT_THREADS = 384;
@@ -767,7 +768,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
 // Experts with at most few_rows rows (single tokens, small batches): the packed
 // codes are decoded into registers as the A fragments of mma.m16n8k16, whose
 // other operand (rows of x) comes from shared memory. What bounds it is issue
-// (decoding, about 1.3 integer operations a code, and the copies' addressing)
+// (decoding, about 1.8 operations a code, and the copies' addressing)
 // before HBM, not the tensor work, so the warp-level instruction fits: no decoded
 // operand passes through shared or tensor memory.
 //
@@ -775,17 +776,18 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gg_tc_kernel(const __grid_const
 // takes 32 of the outputs and every other group. The CTAs of a cluster share the
 // outputs, split the depth and add their sums through distributed shared memory
 // in a fixed order. Codes, x, scales and zeros are one chunk ahead (with a third
-// stage fewer CTAs fit an SM: 247 us instead of 194 on three 13824 x 5120 experts of
+// stage fewer CTAs fit an SM: a quarter more time on three 13824 x 5120 experts of
 // fp32 rows). Of 64 columns (32 in groups of 32) thread (g, t) of a warp takes the
 // 16 (8) codes from 16 t (8 t) on of rows g, g + 8, g + 16, g + 24: as k-steps may
 // take the columns in any order that x follows, those are its pairs of four (two)
 // k-steps, and x's are consecutive bytes. The sums of x over 32 columns are
 // products with rows of ones, a unit of the chunk for each warp.
-// 10.4 us for one row of a 4096 x 4096 layer (5.3 MB), 80 for eight rows over five
-// 11008 x 4096 experts (71 MB, 0.89 TB/s).
+// 10.7 us for one row of a 4096 x 4096 layer (5.3 MB), 84 for eight rows over five
+// 11008 x 4096 experts (71 MB, 0.85 TB/s). (32 rows at a time at groups of 64 and 128
+// spill 28 to 76 bytes at the 128 registers of two CTAs an SM.)
 constexpr int GS_THREADS = 256, GS_M = 128, GS_K = 256, GS_STAGES = 2;
-// What the tables in shared memory hold: the widest layer that the entry point accepts.
 constexpr int GS_SMEM = 160 * 1024;  // beside 32 KB of tables; groups of 32, 7 bits, 16 rows in three planes take 130
+// What the tables in shared memory hold: the widest layer that the entry point accepts.
 constexpr int GS_MAX_CHUNKS = (kMaxColumns + GS_K - 1) / GS_K;
 // Bytes of a row of x: the 16-byte reads of two rows and four threads meet no bank twice.
 __host__ __device__ constexpr int gs_xstride(int group) { return GS_K * 2 + (group == 32 ? 64 : 16); }
@@ -1155,8 +1157,11 @@ __global__ void __launch_bounds__(GS_THREADS, 2) gs_kernel(const GsParams p) {
 
 // ---------------------------------------------------------------- host side
 // Experts with at most this many rows: the few-rows kernel, whose time grows with every 8 rows and starts again
-// every 32, while the other's is the decoding and the depth's chain. Eight 4096 x 4096 experts of 16, 32, 48, 64 rows
-// each: 88, 108, 177, 199 us by the few-rows kernel, 150, 150, 156, 156 by the other.
+// every 32 (fp32 x: 16, each in three planes), while the other's is the decoding and the depth's chain. Eight 4096 x 4096
+// experts of 16, 24, 32, 48, 64 rows each, the few-rows kernel / the other, in us:
+//   bf16, groups of 128: 82/167 108/168 119/168 188/174 209/175    groups of 32: 140/267 163/267 173/267 295/285 312/285
+//   fp32, groups of 128: 110/241 184/241 206/242 296/271 384/272   groups of 32: 196/327 355/330 373/335 544/351 714/358
+// For a single expert the few-rows kernel is the faster one up to 64 rows (fp32 at groups of 32: 48).
 constexpr int kFewRows = 32;
 constexpr size_t kTileBytes = size_t(1) << 30;  // decoded tiles of a pass
 
@@ -1231,8 +1236,9 @@ static cudaError_t launch_few(GsParams p, int64_t slots, int avg_bits, int num_s
   p.cap = GS_K / 32 * std::min(avg_bits + 1, 8) + 4;
   p.wstride = (p.cap + 7) / 8 * 8 + 4;  // 4 modulo 8: the eight rows of a read meet no bank twice
   const size_t smem = (size_t)GS_STAGES * (kPlanes * 8 * kNT * gs_xstride(G) + GS_M * p.wstride * 4);
-  // The depth is split over a cluster until two to four CTAs an SM have work: one row of a 4096 x 4096 layer takes
-  // 10.4 us split over eight and 32.9 whole, 160 rows over seven 4096 x 11008 experts 299 and 330.
+  // The depth is split over a cluster until two to four CTAs an SM have work: one row of a 4096 x 4096 layer takes a
+  // third of the time split over eight (10.4 us against 32.9), 160 rows over seven 4096 x 11008 experts nine tenths. The
+  // host knows how many experts can have rows, not how many have.
   const int64_t tiles = slots * p.mtiles, chunks = (p.n + GS_K - 1) / GS_K;
   int split = 1;
   while (split < 8 && tiles * split * 2 <= (int64_t)num_sms * 4 && chunks >= split * 2) split *= 2;
